@@ -228,7 +228,7 @@ def _recurrence(x, b, h0, gate):
 
 def _recurrence_adjoint(x, h, adj, h0, adj_last, gate):
     a = _gates(x, gate)
-    lam = adj.float()
+    lam = adj.to(torch.float32, copy=True)
     if adj_last is not None:
         lam[:, -1] += adj_last
     nxt = torch.cat([a[:, 1:], torch.zeros_like(a[:, :1])], 1)
