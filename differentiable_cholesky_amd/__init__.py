@@ -45,3 +45,10 @@ from ._lib import (  # noqa: F401
     header_entry_points,
     lib,
 )
+from ._train import (  # noqa: F401
+    CHOL_BF16,
+    CHOL_F16,
+    chol_recurrence,
+    chol_recurrence_adjoint,
+    chol_recurrence_workspace_size,
+)

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "../../include/libchol.h"
+#include "checks.hpp"
 #include "common.hpp"
 #include "plan.hpp"
 #include "profile.hpp"
@@ -87,9 +88,12 @@ const int DEFAULT_NB = 128;
 // Index arithmetic inside the kernels uses 32-bit row/column counts.
 const int64_t MAX_N = (int64_t)1 << 30;
 
-struct Extent {
-    uintptr_t lo, hi; // [lo, hi) in bytes; empty when lo == hi
-};
+using chol::clear_stale_status;
+using chol::Extent;
+using chol::ld_ok;
+using chol::overlap;
+using chol::rect_alias_ok;
+using chol::rect_extent;
 
 bool valid_dtype(chol_dtype dt) { return dt == CHOL_F32 || dt == CHOL_F64; }
 size_t esize(chol_dtype dt) { return dt == CHOL_F64 ? 8 : 4; }
@@ -102,8 +106,6 @@ Extent extent(const void *p, int64_t n, int64_t ld, int64_t batch, int64_t strid
     return e;
 }
 
-bool overlap(const Extent &a, const Extent &b) { return a.lo < b.hi && b.lo < a.hi; }
-
 // Output `o` may be exactly the same buffer as input `i` (same base, ld and
 // stride) or disjoint from it; any other overlap is rejected.
 bool alias_ok(const void *i, int64_t ldi, int64_t si, const void *o, int64_t ldo, int64_t so, int64_t n,
@@ -114,24 +116,6 @@ bool alias_ok(const void *i, int64_t ldi, int64_t si, const void *o, int64_t ldo
     return !overlap(extent(i, n, ldi, batch, si, es), extent(o, n, ldo, batch, so, es));
 }
 
-// rows x cols blocks (right-hand sides of the solve)
-Extent rect_extent(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t batch, int64_t stride, size_t es)
-{
-    Extent e{(uintptr_t)p, (uintptr_t)p};
-    if (rows > 0 && cols > 0 && batch > 0)
-        e.hi = e.lo + (size_t)((batch - 1) * stride + (rows - 1) * ld + cols) * es;
-    return e;
-}
-
-bool rect_alias_ok(const void *i, int64_t ldi, int64_t si, const void *o, int64_t ldo, int64_t so, int64_t rows,
-                   int64_t cols, int64_t batch, size_t es)
-{
-    if (i == o)
-        return ldi == ldo && (batch <= 1 || si == so);
-    return !overlap(rect_extent(i, rows, cols, ldi, batch, si, es), rect_extent(o, rows, cols, ldo, batch, so, es));
-}
-
-bool ld_ok(int64_t ld, int64_t n) { return ld >= std::max<int64_t>(1, n); }
 bool stride_ok(int64_t stride, int64_t ld, int64_t n, int64_t batch)
 {
     return batch <= 1 || stride >= ld * n;
@@ -139,13 +123,6 @@ bool stride_ok(int64_t stride, int64_t ld, int64_t n, int64_t batch)
 bool nb_ok(int64_t nb) { return nb >= 0 && nb <= CHOL_MAX_NB; }
 
 } // namespace
-
-// The library checks each launch with hipGetLastError(), whose status is
-// sticky per host thread: a status left by unrelated HIP calls made earlier on
-// this thread (for example an event query that found work still pending) would
-// be taken for a failed launch.  Every entry point that launches clears it
-// first.
-static inline void clear_stale_status() { (void)hipGetLastError(); }
 
 extern "C" {
 

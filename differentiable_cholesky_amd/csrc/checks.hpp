@@ -1,0 +1,80 @@
+// Host-side argument checks shared by the C-ABI's source files.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstddef>
+#include <cstdint>
+
+namespace chol {
+
+struct Extent {
+    uintptr_t lo, hi; // [lo, hi) in bytes; empty when lo == hi
+};
+
+inline bool overlap(const Extent &a, const Extent &b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// rows x cols blocks (right-hand sides of the solve, rows of a sequence)
+inline Extent rect_extent(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t batch, int64_t stride,
+                          size_t es)
+{
+    Extent e{(uintptr_t)p, (uintptr_t)p};
+    if (rows > 0 && cols > 0 && batch > 0)
+        e.hi = e.lo + (size_t)((batch - 1) * stride + (rows - 1) * ld + cols) * es;
+    return e;
+}
+
+inline bool rect_alias_ok(const void *i, int64_t ldi, int64_t si, const void *o, int64_t ldo, int64_t so, int64_t rows,
+                          int64_t cols, int64_t batch, size_t es)
+{
+    if (i == o)
+        return ldi == ldo && (batch <= 1 || si == so);
+    return !overlap(rect_extent(i, rows, cols, ldi, batch, si, es), rect_extent(o, rows, cols, ldo, batch, so, es));
+}
+
+// A batch of rows x cols blocks that no element belongs to twice: the batch
+// outside the rows, or (sequence-major storage) the rows outside the batch.
+inline bool layout_ok(int64_t rows, int64_t cols, int64_t ld, int64_t batch, int64_t stride)
+{
+    if ((rows > 1 && ld < cols) || (batch > 1 && stride < cols) || ld < 0 || stride < 0)
+        return false;
+    return rows <= 1 || batch <= 1 || stride >= ld * (rows - 1) + cols || ld >= stride * (batch - 1) + cols;
+}
+
+// Whether two such batches share no element.  Blocks whose address ranges
+// interleave (column slices of one joint buffer) are apart if their columns
+// are, counted modulo a row length that both share.
+inline bool apart(const void *p, int64_t ldp, int64_t sp, const void *q, int64_t ldq, int64_t sq, int64_t rows,
+                  int64_t cols, int64_t batch, size_t es)
+{
+    if (!overlap(rect_extent(p, rows, cols, ldp, batch, sp, es), rect_extent(q, rows, cols, ldq, batch, sq, es)))
+        return true;
+    // the period of the rows' addresses: the row length, or the batch's where there is one row
+    const int64_t period = rows > 1 ? ldp : sp;
+    if (ldp != ldq || sp != sq || period <= 0 || (batch > 1 && sp % period != 0))
+        return false;
+    const uintptr_t d = (uintptr_t)p > (uintptr_t)q ? (uintptr_t)p - (uintptr_t)q : (uintptr_t)q - (uintptr_t)p;
+    const int64_t r = (int64_t)(d / es % (uintptr_t)period);
+    return d % es == 0 && r >= cols && r + cols <= period;
+}
+
+// An output over an input: exactly the same elements, or none in common.
+inline bool same_or_apart(const void *i, int64_t ldi, int64_t si, const void *o, int64_t ldo, int64_t so, int64_t rows,
+                          int64_t cols, int64_t batch, size_t es)
+{
+    if (i == o)
+        return (rows <= 1 || ldi == ldo) && (batch <= 1 || si == so);
+    return apart(i, ldi, si, o, ldo, so, rows, cols, batch, es);
+}
+
+inline bool ld_ok(int64_t ld, int64_t n) { return ld >= std::max<int64_t>(1, n); }
+
+// The library checks each launch with hipGetLastError(), whose status is
+// sticky per host thread: a status left by unrelated HIP calls made earlier on
+// this thread (for example an event query that found work still pending) would
+// be taken for a failed launch.  Every entry point that launches clears it
+// first.
+inline void clear_stale_status() { (void)hipGetLastError(); }
+
+} // namespace chol

@@ -78,10 +78,18 @@ extern "C" {
  * lengthen the serial chain of diagonal factors that the updates hide. */
 #define CHOL_MAX_NB 128
 
-/* Real types for every entry point; the complex types (interleaved real and
+/* Real types (fp32, fp64) for the factor, its adjoint and the solves; the complex types (interleaved real and
  * imaginary parts, complex64 = 2 x fp32, complex128 = 2 x fp64) only for the
- * chol_potrf_hermitian* family. */
-typedef enum { CHOL_F32 = 0, CHOL_F64 = 1, CHOL_C64 = 2, CHOL_C128 = 3 } chol_dtype;
+ * chol_potrf_hermitian* family; the 16-bit types, and fp32, for the training
+ * operators (chol_recurrence*). */
+typedef enum {
+    CHOL_F32 = 0,
+    CHOL_F64 = 1,
+    CHOL_C64 = 2,
+    CHOL_C128 = 3,
+    CHOL_BF16 = 4,
+    CHOL_F16 = 5
+} chol_dtype;
 
 typedef enum {
     CHOL_OK = 0,
@@ -414,6 +422,71 @@ chol_status chol_potrs_adjoint_batched(chol_dtype dtype, int64_t n, int64_t nrhs
                                        void *adjL, int64_t ldal, int64_t strideAL,
                                        int accumulate, void *stream);
 
+/* How chol_recurrence's gates are stored: as they multiply the state, or as
+ * their logarithm (the gate is exp of the element; -inf closes it). */
+#define CHOL_GATE_LINEAR 0
+#define CHOL_GATE_LOG 1
+
+/*
+ * chol_recurrence -- the gated linear recurrence
+ *     h_t = a_t h_{t-1} + b_t,   t = 0 .. len-1,
+ * for every channel of a [batch, len, dim] sequence on its own.
+ *   dtype  CHOL_F32, CHOL_BF16 or CHOL_F16, of a, b and h.  The state is fp32
+ *          throughout; h rounds it once per element.
+ *   gate   CHOL_GATE_LINEAR: a holds a_t; CHOL_GATE_LOG: a holds log a_t.
+ *   a, b   [in]  device; element (i, t, c) at p[i * stride + t * ld + c].  The
+ *          batch may lie outside the rows (stride >= ld * (len-1) + dim) or,
+ *          in sequence-major storage, inside (ld >= stride * (batch-1) + dim).
+ *   h0     [in]  device fp32 [batch, dim], the state before the first step;
+ *          NULL is zero.
+ *   hlast  [out] device fp32 [batch, dim], the state after the last step.
+ *          hlast == h0 updates a kept state in place (decoding: len = 1).
+ *          len = 0 copies h0.
+ *   h      [out] device, laid out like a and b.  h may be a or b itself (same
+ *          ld and stride); otherwise it shares no element with them.  Column
+ *          slices of one joint buffer with the same ld and stride are apart.
+ *   workspace  at least chol_recurrence_workspace_size bytes (8-byte aligned;
+ *          NULL allowed when it is 0).
+ * The products of consecutive gates are formed in fp32: gates of magnitude at
+ * most 1 are what the segmented form is meant for; where a run of larger ones
+ * overflows, the result is inf or NaN.
+ * batch * dim above 2^31 - 1 returns CHOL_ERR_NOT_SUPPORTED.
+ */
+chol_status chol_recurrence(chol_dtype dtype, int gate, int64_t batch, int64_t len, int64_t dim,
+                            const void *a, int64_t lda, int64_t strideA,
+                            const void *b, int64_t ldb, int64_t strideB,
+                            const float *h0, float *hlast,
+                            void *h, int64_t ldh, int64_t strideH,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * chol_recurrence_adjoint -- reverse-mode adjoint of chol_recurrence.  With
+ *     lam_t = adjH_t + a_{t+1} lam_{t+1},   lam_{len-1} = adjH_{len-1} + adjHlast,
+ * it writes
+ *     adjB_t = lam_t,   adjA_t = lam_t h_{t-1} (times a_t for CHOL_GATE_LOG: the
+ *     gradient of the stored logarithm),   adjH0 = a_0 lam_0.
+ *   a, h     [in] the gates, and the states chol_recurrence wrote (h_{t-1} at
+ *            t = 0 is h0, or zero when h0 is NULL).
+ *   adjH     [in] gradient of h; adjHlast [in] fp32 [batch, dim], gradient of
+ *            hlast, or NULL for zero.
+ *   adjA, adjB  [out] may be a or adjH themselves (not h, and apart from each
+ *            other); adjH0 [out] fp32 [batch, dim], may be adjHlast itself.
+ * Layouts, workspace and limits as chol_recurrence.
+ */
+chol_status chol_recurrence_adjoint(chol_dtype dtype, int gate, int64_t batch, int64_t len, int64_t dim,
+                                    const void *a, int64_t lda, int64_t strideA,
+                                    const void *h, int64_t ldh, int64_t strideH,
+                                    const void *adjH, int64_t ldah, int64_t strideAH,
+                                    const float *h0, const float *adjHlast,
+                                    void *adjA, int64_t ldaa, int64_t strideAA,
+                                    void *adjB, int64_t ldab, int64_t strideAB,
+                                    float *adjH0,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace chol_recurrence and chol_recurrence_adjoint need. */
+chol_status chol_recurrence_workspace_size(chol_dtype dtype, int64_t batch, int64_t len, int64_t dim,
+                                           size_t *bytes);
+
 /*
  * chol_wave_dot_fwd_adj -- diagnostic kernel for the reduction/broadcast
  * pattern the small-tile kernels rely on (Warp issue #1374, "adj_tile_dot is
@@ -486,7 +559,9 @@ typedef enum {
     CHOL_K_SOLVE = 12,           /* chol_potrs*, and the solve inside chol_potrs_adjoint*, whole
                                     calls; flops: 2 n^2 nrhs per matrix */
     CHOL_K_SOLVE_ADJOINT = 13,   /* the adj_L term of chol_potrs_adjoint*; flops: 4 n^2 nrhs per matrix */
-    CHOL_K_COUNT = 14
+    CHOL_K_RECURRENCE = 14,      /* chol_recurrence, whole calls; bytes: 3 * batch * len * dim * elem */
+    CHOL_K_RECURRENCE_ADJOINT = 15, /* chol_recurrence_adjoint, whole calls; bytes: 5 * batch * len * dim * elem */
+    CHOL_K_COUNT = 16
 } chol_kernel_family;
 
 #define CHOL_PROFILE_ALL 0xffffffffu
