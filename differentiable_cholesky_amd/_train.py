@@ -19,6 +19,12 @@ GATES = {"linear": 0, "log": 1}
 _CODES = {torch.float32: CHOL_F32, torch.bfloat16: CHOL_BF16, torch.float16: CHOL_F16}
 
 
+class AdamwTensor(ctypes.Structure):
+    """chol_adamw_tensor"""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("p", "g", "m", "v", "master", "m_scale", "v_scale")] + \
+               [(k, ctypes.c_int64) for k in ("n", "first")]
+
+
 def _bind():
     i64, i32, vp, sz = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
     rows = [vp, i64, i64]
@@ -26,6 +32,16 @@ def _bind():
     lib.chol_recurrence_adjoint.argtypes = [i32, i32, i64, i64, i64, *rows, *rows, *rows, vp, vp, *rows, *rows, vp,
                                             vp, sz, vp]
     lib.chol_recurrence_workspace_size.argtypes = [i32, i64, i64, i64, ctypes.POINTER(sz)]
+    lib.chol_rmsnorm.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, ctypes.c_float, vp, i64, vp, i64, vp]
+    lib.chol_rmsnorm_quant.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, vp, ctypes.c_float, vp, i64, vp, i64, vp,
+                                       i64, vp]
+    lib.chol_rmsnorm_adjoint.argtypes = [i32, i64, i64, vp, i64, vp, vp, i64, vp, i64, ctypes.c_float, vp, i64, vp,
+                                         i32, vp, sz, vp]
+    lib.chol_rmsnorm_adjoint_workspace_size.argtypes = [i32, i64, i64, ctypes.POINTER(sz)]
+    f64 = ctypes.c_double
+    lib.chol_adamw_list.argtypes = [i32, i32, i64, ctypes.POINTER(AdamwTensor), vp, sz, ctypes.POINTER(i64),
+                                    ctypes.POINTER(sz)]
+    lib.chol_adamw.argtypes = [i32, i32, i32, i64, vp, vp, f64, f64, f64, f64, f64, i64, ctypes.c_uint32, vp]
 
 
 _bind()
@@ -186,3 +202,221 @@ def chol_recurrence_adjoint(a, h, adjH, h0=None, adjHlast=None, adjA=None, adjB=
                                            *_seq(adjH, "adjH"), ph0, pl, *_seq(adjA, "adjA"), *_seq(adjB, "adjB"), p0,
                                            ws, wbytes, _raw_stream(a)))
     return adjA, adjB, adjH0
+
+
+# ---------------------------------------------------------------- RMS norm ----
+
+RMSNORM_GROUPS = (0, 32, 64, 128, 256)
+
+
+def _rows(t, name: str):
+    """(pointer, ld) of a [rows, cols] array with unit column stride, or of any
+    contiguous array taken as rows of its last dimension."""
+    if t.dim() == 2:
+        ld, sc = t.stride()
+        rows, cols = t.shape
+        if cols > 1 and sc != 1:
+            raise ValueError(f"{name} must have unit column stride")
+        return t.data_ptr(), ld if rows > 1 else cols
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be [rows, cols] or contiguous")
+    return t.data_ptr(), t.shape[-1]
+
+
+def _row_shape(x, w):
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    cols = x.shape[-1]
+    _same(w, "w", x, (cols,))
+    if not w.is_contiguous():
+        raise ValueError("w must be contiguous")
+    return (x.shape[0] if x.dim() == 2 else x.numel() // cols if cols else 0), cols
+
+
+def chol_rmsnorm(x, w, residual=None, eps: float = 1e-6, y=None, h=None, stream=None):
+    """y = h w / sqrt(mean(h^2) + eps) over the last dimension, h = x + residual:
+    returns (y, h), where h is x itself without a residual.  ``y`` or ``h`` may
+    be ``x`` or ``residual`` (in place)."""
+    code = _code(x)
+    rows, cols = _row_shape(x, w)
+    with _on(x, stream):
+        px, ldx = _rows(x, "x")
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            _same(y, "y", x)
+        py, ldy = _rows(y, "y")
+        pr = ph = None
+        ldr = ldh = cols
+        if residual is None:
+            h = x
+        else:
+            _same(residual, "residual", x)
+            pr, ldr = _rows(residual, "residual")
+            if h is None:
+                h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            else:
+                _same(h, "h", x)
+            ph, ldh = _rows(h, "h")
+        _check(lib.chol_rmsnorm(code, rows, cols, px, ldx, pr, ldr, w.data_ptr(), eps, py, ldy, ph, ldh,
+                                _raw_stream(x)))
+    return y, h
+
+
+def chol_rmsnorm_quant(x, w, residual=None, group: int = 0, eps: float = 1e-6, q=None, scale=None, h=None,
+                       stream=None):
+    """chol_rmsnorm with y as float8_e4m3fn and fp32 scales, one for every
+    ``group`` columns (0: one a row): returns (q, scale, h) with y ~ q * scale.
+    ``scale`` is [rows, ceil(cols / group)]."""
+    code = _code(x)
+    rows, cols = _row_shape(x, w)
+    if group not in RMSNORM_GROUPS:
+        raise ValueError(f"group must be one of {RMSNORM_GROUPS}, got {group}")
+    groups = -(-cols // group) if group else 1
+    with _on(x, stream):
+        px, ldx = _rows(x, "x")
+        if q is None:
+            q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        else:
+            _same(q, "q", x, dtype=torch.float8_e4m3fn)
+        if scale is None:
+            scale = torch.empty((rows, groups), dtype=torch.float32, device=x.device)
+        else:
+            _same(scale, "scale", x, (rows, groups), torch.float32)
+        pq, ldq = _rows(q, "q")
+        ps, lds = _rows(scale, "scale")
+        pr = ph = None
+        ldr = ldh = cols
+        if residual is None:
+            h = x
+        else:
+            _same(residual, "residual", x)
+            pr, ldr = _rows(residual, "residual")
+            if h is None:
+                h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            else:
+                _same(h, "h", x)
+            ph, ldh = _rows(h, "h")
+        _check(lib.chol_rmsnorm_quant(code, rows, cols, group, px, ldx, pr, ldr, w.data_ptr(), eps, pq, ldq, ps, lds,
+                                      ph, ldh, _raw_stream(x)))
+    return q, scale, h
+
+
+def chol_rmsnorm_adjoint_workspace_size(dtype_code: int, rows: int, cols: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib.chol_rmsnorm_adjoint_workspace_size(dtype_code, rows, cols, ctypes.byref(out)))
+    return int(out.value)
+
+
+def chol_rmsnorm_adjoint(h, w, adj, adjH=None, eps: float = 1e-6, adjX=None, adjW=None, accumulate: bool = False,
+                         workspace=None, stream=None):
+    """Adjoint of chol_rmsnorm: returns (adjX, adjW).  ``adj`` is the gradient of
+    y, ``adjH`` the one that reaches h past the norm; adjX is the gradient of h, so
+    of x and of the residual.  ``adjW`` (fp32) is added to with ``accumulate``."""
+    code = _code(h)
+    rows, cols = _row_shape(h, w)
+    _same(adj, "adj", h)
+    with _on(h, stream):
+        if adjX is None:
+            adjX = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+        else:
+            _same(adjX, "adjX", h)
+        if adjW is None:
+            adjW = (torch.zeros if accumulate else torch.empty)((cols,), dtype=torch.float32, device=h.device)
+        else:
+            _state(adjW, "adjW", h, (cols,))
+        ph, ldh = _rows(h, "h")
+        pa, lda = _rows(adj, "adj")
+        pg, ldg = None, cols
+        if adjH is not None:
+            _same(adjH, "adjH", h)
+            pg, ldg = _rows(adjH, "adjH")
+        px, ldx = _rows(adjX, "adjX")
+        keep, ws, wbytes = _scratch(chol_rmsnorm_adjoint_workspace_size(code, rows, cols), h.device, workspace)
+        _check(lib.chol_rmsnorm_adjoint(code, rows, cols, ph, ldh, w.data_ptr(), pa, lda, pg, ldg, eps, px, ldx,
+                                        adjW.data_ptr(), 1 if accumulate else 0, ws, wbytes, _raw_stream(h)))
+    return adjX, adjW
+
+
+# ------------------------------------------------------------------- AdamW ----
+
+ADAMW_TILE = 256
+
+
+class AdamwList:
+    """The tensors of an AdamW step and their work list on the device.  Holds the
+    tensors, whose memory the list addresses."""
+
+    def __init__(self, code, bits, master, chunks, table, tensors):
+        self.code, self.bits, self.master, self.chunks = code, bits, master, chunks
+        self.table, self.tensors = table, tensors
+
+
+def chol_adamw_list(p, g, m, v, master=None, m_scale=None, v_scale=None, first=None) -> AdamwList:
+    """The work list of chol_adamw, made once for lists of contiguous tensors.
+
+    p, g: weights and gradients of one type.  m, v: states, all float32, or all
+    float8_e4m3fn with ``m_scale`` and ``v_scale`` (fp32, one for every 256
+    elements; v then holds the root of the second moment).  ``master``: fp32
+    weights that p is the rounding of.  ``first``: each tensor's position in the
+    random sequence (default: one after the other, each rounded up to 256)."""
+    p, g, m, v = list(p), list(g), list(m), list(v)
+    if not p:
+        raise ValueError("the list has no tensors")
+    bits = {torch.float32: 32, torch.float8_e4m3fn: 8}.get(m[0].dtype)
+    if bits is None:
+        raise TypeError(f"states must be float32 or float8_e4m3fn, got {m[0].dtype}")
+    if bits == 8 and (m_scale is None or v_scale is None):
+        raise ValueError("8-bit states need m_scale and v_scale")
+    if bits == 32 and (m_scale is not None or v_scale is not None):
+        raise ValueError("32-bit states take no scales")
+    code = _code(p[0])
+    if not p[0].is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    columns = {"p": (p, p[0].dtype), "g": (g, p[0].dtype), "m": (m, m[0].dtype), "v": (v, m[0].dtype)}
+    for name, given in (("master", master), ("m_scale", m_scale), ("v_scale", v_scale)):
+        if given is not None:
+            columns[name] = (list(given), torch.float32)
+    items = (AdamwTensor * len(p))()
+    at = 0
+    if first is not None:
+        first = list(first)
+        if len(first) != len(p):
+            raise ValueError(f"first has {len(first)} entries for {len(p)} tensors")
+    for name, (tensors, dtype) in columns.items():
+        if len(tensors) != len(p):
+            raise ValueError(f"{name} has {len(tensors)} tensors for {len(p)}")
+        for i, t in enumerate(tensors):
+            n = p[i].numel()
+            _same(t, f"{name}[{i}]", p[0], t.shape, dtype)
+            if t.numel() != (-(-n // ADAMW_TILE) if name.endswith("_scale") else n):
+                raise ValueError(f"{name}[{i}] has {t.numel()} elements for {n} weights")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be contiguous")
+            setattr(items[i], name, t.data_ptr())
+    for i, t in enumerate(p):
+        items[i].n = t.numel()
+        items[i].first = at if first is None else first[i]
+        at += -(-t.numel() // ADAMW_TILE) * ADAMW_TILE
+    chunks, size = ctypes.c_int64(0), ctypes.c_size_t(0)
+    _check(lib.chol_adamw_list(code, bits, len(p), items, None, 0, ctypes.byref(chunks), ctypes.byref(size)))
+    host = torch.empty(max(size.value, 8), dtype=torch.uint8)
+    _check(lib.chol_adamw_list(code, bits, len(p), items, host.data_ptr(), host.numel(), ctypes.byref(chunks),
+                               ctypes.byref(size)))
+    return AdamwList(code, bits, int(master is not None), chunks.value, host.to(p[0].device),
+                     [c[0] for c in columns.values()])
+
+
+def chol_adamw(tensors: AdamwList, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.0, grad_scale=None, seed: int = 0, stream=None) -> None:
+    """One AdamW step over the list, in place.  ``grad_scale``: fp32 device tensor
+    of one element that gradients are multiplied by.  ``seed``: this step's random
+    roundings of 8-bit states (another one each step)."""
+    if grad_scale is not None:
+        if grad_scale.numel() != 1:
+            raise ValueError("grad_scale must have one element")
+        _same(grad_scale, "grad_scale", tensors.table, grad_scale.shape, torch.float32)
+    with _on(tensors.table, stream):
+        _check(lib.chol_adamw(tensors.code, tensors.bits, tensors.master, tensors.chunks, tensors.table.data_ptr(),
+                              _ptr(grad_scale), lr, beta1, beta2, eps, weight_decay, step, seed & 0xFFFFFFFF,
+                              _raw_stream(tensors.table)))

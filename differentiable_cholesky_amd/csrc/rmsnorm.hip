@@ -1,0 +1,396 @@
+// RMS norm with the residual's addition, an output in the input's type or in
+// e4m3 with scales, and the adjoint.
+//
+//   h = rnd(x + r),  s = (mean h^2 + eps)^(-1/2),  y = h s w
+//   adj_x = s (g - h s^2 mean(g h)) + adj_h with g = adj w,  adj_w = sum_rows adj h s
+//
+// A row stays in the registers of TPR threads, NV vectors of 16 bytes each, so
+// the data is read once and written once, which is what bounds these kernels.
+// Sums and maxima cross the lanes of a wave by shuffles and waves through LDS.
+#include <algorithm>
+#include <type_traits>
+
+#include "lowp.hpp"
+#include "rmsnorm.hpp"
+
+namespace chol {
+
+namespace {
+
+constexpr int WAVE = 64;
+constexpr float E4M3_MAX = 448.f;
+// blocks of the adjoint's grid: each leaves one row of partial sums of adj_w
+constexpr int ADJ_BLOCKS = 512;
+
+template <typename T> constexpr int vec_of = 16 / (int)sizeof(T);
+
+// NV vectors of one row, thread `t` of TPR holding vectors t, t + TPR, ...; zero
+// past the end of the row.
+template <typename T, int TPR, int NV> struct Row {
+    static constexpr int V = vec_of<T>;
+    vec<T, V> v[NV];
+    __device__ __forceinline__ void load(const T *p, int t, int cols)
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * V;
+            if (c + V <= cols) {
+                v[i] = load_vec<T, V>(p + c);
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    v[i][k] = c + k < cols ? p[c + k] : (T)0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T *p, int t, int cols) const
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * V;
+            if (c + V <= cols) {
+                store_vec<T, V>(p + c, v[i]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (c + k < cols)
+                        p[c + k] = v[i][k];
+            }
+        }
+    }
+    __device__ __forceinline__ float at(int i, int k) const { return (float)v[i][k]; }
+    __device__ __forceinline__ void set(int i, int k, float x) { v[i][k] = (T)x; }
+};
+
+struct Sum {
+    static __device__ __forceinline__ float of(float a, float b) { return a + b; }
+};
+// largest magnitude by its bits: as integers, finite < inf < NaN
+struct MaxBits {
+    static __device__ __forceinline__ unsigned of(unsigned a, unsigned b) { return a > b ? a : b; }
+};
+
+// Over the TPR threads of a row (all of them get the result).  `slot`: LDS of
+// TPR / WAVE values of this row's own, not used by the call before.
+template <int TPR, typename Op, typename S> __device__ __forceinline__ S over_row(S x, int t, S *slot)
+{
+#pragma unroll
+    for (int o = WAVE / 2; o > 0; o /= 2)
+        x = Op::of(x, __shfl_xor(x, o));
+    if constexpr (TPR > WAVE) {
+        if (t % WAVE == 0)
+            slot[t / WAVE] = x;
+        __syncthreads();
+        x = slot[0];
+#pragma unroll
+        for (int i = 1; i < TPR / WAVE; ++i)
+            x = Op::of(x, slot[i]);
+    }
+    return x;
+}
+
+// e4m3 codes of V values, to nearest even, at a byte address
+template <int V> __device__ __forceinline__ void store_e4m3(unsigned char *p, const float (&q)[V], int n)
+{
+    unsigned word[V / 4];
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) {
+        int u = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * k], q[4 * k + 1], 0, false);
+        word[k] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * k + 2], q[4 * k + 3], u, true);
+    }
+    if (n >= V) {
+        __builtin_memcpy(p, word, V);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (k < n)
+                p[k] = (unsigned char)(word[k / 4] >> (8 * (k % 4)));
+    }
+}
+
+template <typename T, int TPR, int NV, bool QUANT>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
+{
+    constexpr int V = vec_of<T>, BLOCK = TPR < 256 ? 256 : TPR;
+    __shared__ float s_sum[TPR > WAVE ? TPR / WAVE : 1];
+    __shared__ unsigned s_max[TPR > WAVE ? TPR / WAVE : 1];
+    const int t = threadIdx.x % TPR, cols = (int)a.cols;
+    const int64_t row = (int64_t)blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;
+    if (row >= a.rows) // whole waves; rows of more than a wave fill their block
+        return;
+    Row<T, TPR, NV> h, w;
+    h.load((const T *)a.x + row * a.ldx, t, cols);
+    if (a.residual) {
+        Row<T, TPR, NV> r;
+        r.load((const T *)a.residual + row * a.ldr, t, cols);
+        w.load((const T *)a.w, t, cols);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                h.set(i, k, h.at(i, k) + r.at(i, k));
+        h.store((T *)a.h + row * a.ldh, t, cols);
+    } else {
+        w.load((const T *)a.w, t, cols);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            sum = fmaf(h.at(i, k), h.at(i, k), sum);
+    const float s = rsqrtf(over_row<TPR, Sum>(sum, t, s_sum) / (float)cols + a.eps);
+    if constexpr (!QUANT) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                h.set(i, k, h.at(i, k) * s * w.at(i, k));
+        h.store((T *)a.y + row * a.ldy, t, cols);
+    } else {
+        float y[NV][V];
+        unsigned most[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            most[i] = 0;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                y[i][k] = h.at(i, k) * s * w.at(i, k);
+                most[i] = MaxBits::of(most[i], __float_as_uint(y[i][k]) & 0x7fffffffu);
+            }
+        }
+        if (a.group) {
+            // a group is `lanes` neighbouring vectors of one wave
+            const int lanes = a.group / V;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                for (int o = 1; o < lanes; o *= 2)
+                    most[i] = MaxBits::of(most[i], __shfl_xor(most[i], o));
+        } else {
+#pragma unroll
+            for (int i = 1; i < NV; ++i)
+                most[0] = MaxBits::of(most[0], most[i]);
+            most[0] = over_row<TPR, MaxBits>(most[0], t, s_max);
+        }
+        unsigned char *q = (unsigned char *)a.y + row * a.ldy;
+        float *scale = a.scale + row * a.lds;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * V;
+            const unsigned m = a.group ? most[i] : most[0];
+            // one for a group of zeros (or with a NaN); not below the smallest
+            // normal number, whose reciprocal still is one
+            const float sc = m == 0 || m > 0x7f800000u ? 1.f : fmaxf(__uint_as_float(m) * (1.f / E4M3_MAX), 0x1p-126f);
+            const float inv = __frcp_rn(sc);
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                y[i][k] *= inv;
+            if (c < cols) {
+                store_e4m3<V>(q + c, y[i], cols - c);
+                if (a.group ? c % a.group == 0 : c == 0)
+                    scale[a.group ? c / a.group : 0] = sc;
+            }
+        }
+    }
+}
+
+// Rows blockIdx.x * RPB + slot, then a grid further on; every thread sums its
+// columns' adj h s over its rows.  part[blockIdx.x * cols + c], or adj_w itself
+// where the grid is one block.
+template <typename T, int TPR, int NV>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm_adjoint(NormAdjArgs a, float *part)
+{
+    constexpr int V = vec_of<T>, BLOCK = TPR < 256 ? 256 : TPR, RPB = BLOCK / TPR;
+    __shared__ float s_sum[2][TPR > WAVE ? 2 * TPR / WAVE : 1];
+    __shared__ float s_w[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? TPR * NV * V : 1];
+    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR, cols = (int)a.cols;
+    Row<T, TPR, NV> w;
+    w.load((const T *)a.w, t, cols);
+    float acc[NV][V] = {};
+    int phase = 0;
+    for (int64_t row = (int64_t)blockIdx.x * RPB + slot; row < a.rows; row += (int64_t)gridDim.x * RPB, phase ^= 1) {
+        Row<T, TPR, NV> h, g, p;
+        h.load((const T *)a.h + row * a.ldh, t, cols);
+        g.load((const T *)a.adj + row * a.lda, t, cols);
+        if (a.adj_h)
+            p.load((const T *)a.adj_h + row * a.ldah, t, cols);
+        float hh = 0.f, gh = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                hh = fmaf(h.at(i, k), h.at(i, k), hh);
+                gh = fmaf(g.at(i, k) * w.at(i, k), h.at(i, k), gh);
+            }
+#pragma unroll
+        for (int o = WAVE / 2; o > 0; o /= 2) {
+            hh += __shfl_xor(hh, o);
+            gh += __shfl_xor(gh, o);
+        }
+        if constexpr (TPR > WAVE) {
+            constexpr int W = TPR / WAVE;
+            // two sets in turn: a wave that is a row ahead writes the other one
+            if (t % WAVE == 0) {
+                s_sum[phase][t / WAVE] = hh;
+                s_sum[phase][W + t / WAVE] = gh;
+            }
+            __syncthreads();
+            hh = gh = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                hh += s_sum[phase][i];
+                gh += s_sum[phase][W + i];
+            }
+        }
+        const float n = (float)cols, s = rsqrtf(hh / n + a.eps), along = s * s * (gh / n);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float hv = h.at(i, k), gv = g.at(i, k);
+                acc[i][k] = fmaf(gv, hv * s, acc[i][k]);
+                float d = s * (gv * w.at(i, k) - hv * along);
+                if (a.adj_h)
+                    d += p.at(i, k);
+                h.set(i, k, d);
+            }
+        h.store((T *)a.adj_x + row * a.ldax, t, cols);
+    }
+    if constexpr (RPB > 1) {
+        if (slot > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    s_w[slot - 1][(i * TPR + t) * V + k] = acc[i][k];
+        }
+        __syncthreads();
+        if (slot > 0)
+            return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+#pragma unroll
+                for (int j = 0; j < RPB - 1; ++j)
+                    acc[i][k] += s_w[j][(i * TPR + t) * V + k];
+    }
+    const bool one = gridDim.x == 1;
+    float *out = one ? a.adj_w : part + (int64_t)blockIdx.x * cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (i * TPR + t) * V + k;
+            if (c < cols)
+                out[c] = one && a.accumulate ? out[c] + acc[i][k] : acc[i][k];
+        }
+}
+
+// adj_w[c] (+)= the sum of `count` rows of partial sums, in a fixed order: 16
+// waves take every 16th row, and their sums are added in LDS.
+__global__ void __launch_bounds__(1024) k_sum_rows(const float *part, int count, int cols, float *out, int accumulate)
+{
+    __shared__ float s[16][WAVE];
+    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE, c = (int)blockIdx.x * WAVE + lane;
+    float x = 0.f;
+    if (c < cols)
+#pragma unroll 8
+        for (int r = wave; r < count; r += 16)
+            x += part[(int64_t)r * cols + c];
+    s[wave][lane] = x;
+    __syncthreads();
+    if (wave == 0 && c < cols) {
+        for (int i = 1; i < 16; ++i)
+            x += s[i][lane];
+        out[c] = accumulate ? out[c] + x : x;
+    }
+}
+
+// no rows: adj_w has no terms
+__global__ void __launch_bounds__(256) k_zero(float *out, int n)
+{
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i < n)
+        out[i] = 0.f;
+}
+
+// Runs f(threads of a row, vectors of a thread) for rows of `n` vectors
+template <typename F> chol_status with_shape(int64_t n, F f)
+{
+    using std::integral_constant;
+    if (n <= 64) return f(integral_constant<int, 64>(), integral_constant<int, 1>());
+    if (n <= 128) return f(integral_constant<int, 64>(), integral_constant<int, 2>());
+    if (n <= 256) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
+    if (n <= 512) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
+    if (n <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
+    if (n <= 2048) return f(integral_constant<int, 1024>(), integral_constant<int, 2>());
+    if (n <= 4096) return f(integral_constant<int, 1024>(), integral_constant<int, 4>());
+    return CHOL_ERR_NOT_SUPPORTED;
+}
+
+template <typename T> int64_t vectors(int64_t cols) { return (cols + vec_of<T> - 1) / vec_of<T>; }
+
+int64_t adjoint_blocks(int64_t rows, int rpb) { return std::min<int64_t>(ADJ_BLOCKS, (rows + rpb - 1) / rpb); }
+
+} // namespace
+
+chol_status rmsnorm(chol_dtype dt, bool quantise, const NormArgs &a, hipStream_t st)
+{
+    return with_lowp(dt, [&](auto *e) {
+        typedef std::remove_pointer_t<decltype(e)> T;
+        return with_shape(vectors<T>(a.cols), [&](auto tpr, auto nv) {
+            constexpr int TPR = tpr, NV = nv, BLOCK = TPR < 256 ? 256 : TPR;
+            const int64_t grid = (a.rows + BLOCK / TPR - 1) / (BLOCK / TPR);
+            if (quantise)
+                hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, true>), dim3((unsigned)grid), dim3(BLOCK), 0, st, a);
+            else
+                hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, false>), dim3((unsigned)grid), dim3(BLOCK), 0, st, a);
+            CHOL_LAUNCH_CHECK();
+            return CHOL_OK;
+        });
+    });
+}
+
+size_t rmsnorm_adjoint_workspace(chol_dtype dt, int64_t rows, int64_t cols)
+{
+    size_t bytes = 0;
+    (void)with_lowp(dt, [&](auto *e) {
+        typedef std::remove_pointer_t<decltype(e)> T;
+        return with_shape(vectors<T>(cols), [&](auto tpr, auto) {
+            constexpr int TPR = tpr, RPB = TPR < 256 ? 256 / TPR : 1;
+            const int64_t blocks = adjoint_blocks(rows, RPB);
+            bytes = blocks > 1 ? (size_t)(blocks * cols) * sizeof(float) : 0;
+            return CHOL_OK;
+        });
+    });
+    return bytes;
+}
+
+chol_status rmsnorm_adjoint(chol_dtype dt, const NormAdjArgs &a, void *ws, hipStream_t st)
+{
+    if (a.rows == 0) {
+        if (!a.accumulate)
+            hipLaunchKernelGGL(k_zero, dim3((unsigned)((a.cols + 255) / 256)), dim3(256), 0, st, a.adj_w, (int)a.cols);
+        CHOL_LAUNCH_CHECK();
+        return CHOL_OK;
+    }
+    return with_lowp(dt, [&](auto *e) {
+        typedef std::remove_pointer_t<decltype(e)> T;
+        return with_shape(vectors<T>(a.cols), [&](auto tpr, auto nv) {
+            constexpr int TPR = tpr, NV = nv, BLOCK = TPR < 256 ? 256 : TPR;
+            const int64_t blocks = adjoint_blocks(a.rows, BLOCK / TPR);
+            hipLaunchKernelGGL((k_rmsnorm_adjoint<T, TPR, NV>), dim3((unsigned)blocks), dim3(BLOCK), 0, st, a,
+                               (float *)ws);
+            CHOL_LAUNCH_CHECK();
+            if (blocks > 1) {
+                hipLaunchKernelGGL(k_sum_rows, dim3((unsigned)((a.cols + WAVE - 1) / WAVE)), dim3(1024), 0, st,
+                                   (const float *)ws, (int)blocks, (int)a.cols, a.adj_w, a.accumulate);
+                CHOL_LAUNCH_CHECK();
+            }
+            return CHOL_OK;
+        });
+    });
+}
+
+} // namespace chol

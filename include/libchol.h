@@ -81,7 +81,7 @@ extern "C" {
 /* Real types (fp32, fp64) for the factor, its adjoint and the solves; the complex types (interleaved real and
  * imaginary parts, complex64 = 2 x fp32, complex128 = 2 x fp64) only for the
  * chol_potrf_hermitian* family; the 16-bit types, and fp32, for the training
- * operators (chol_recurrence*). */
+ * operators (chol_recurrence*, chol_rmsnorm*, chol_adamw*). */
 typedef enum {
     CHOL_F32 = 0,
     CHOL_F64 = 1,
@@ -487,6 +487,129 @@ chol_status chol_recurrence_adjoint(chol_dtype dtype, int gate, int64_t batch, i
 chol_status chol_recurrence_workspace_size(chol_dtype dtype, int64_t batch, int64_t len, int64_t dim,
                                            size_t *bytes);
 
+/* Longest row of the RMS norm: a row stays in one workgroup's registers. */
+#define CHOL_RMSNORM_MAX_COLS 16384
+
+/*
+ * chol_rmsnorm -- RMS norm of the rows of x, with the residual's addition:
+ *     h = x + residual (rounded to dtype; h = x without a residual),
+ *     y = h w / sqrt(mean(h^2) + eps).
+ *   dtype     CHOL_F32, CHOL_BF16 or CHOL_F16, of every array; sums in fp32.
+ *   rows, cols  cols <= CHOL_RMSNORM_MAX_COLS (more returns
+ *             CHOL_ERR_NOT_SUPPORTED); rows == 0 or cols == 0 is a no-op.
+ *   x         [in]  device, rows of leading dimension ldx (>= cols).
+ *   residual  [in]  device, or NULL.
+ *   w         [in]  device, cols elements.
+ *   y         [out] device; may be x or residual itself.
+ *   h         [out] device; may be x or residual itself (not y).  Not used, and
+ *             may be NULL, without a residual.
+ * Outputs otherwise share no element with inputs or each other.
+ */
+chol_status chol_rmsnorm(chol_dtype dtype, int64_t rows, int64_t cols,
+                         const void *x, int64_t ldx,
+                         const void *residual, int64_t ldr,
+                         const void *w, float eps,
+                         void *y, int64_t ldy,
+                         void *h, int64_t ldh, void *stream);
+
+/*
+ * chol_rmsnorm_quant -- chol_rmsnorm with y in 8 bits (e4m3, largest value 448):
+ *     scale = max |y| / 448 over a group,   q = e4m3(y / scale), to nearest even.
+ *   group  columns that share a scale: 32, 64, 128 or 256 (the last group of a
+ *          row may be shorter), or 0 for one scale a row.
+ *   q      [out] device, one byte an element, leading dimension ldq.
+ *   scale  [out] device fp32, ceil(cols / group) a row (1 for group 0), leading
+ *          dimension lds.  1 where the group's values are all zero or one is
+ *          NaN (that element's code is NaN then); never below 2^-126.
+ * Other arguments as chol_rmsnorm.
+ */
+chol_status chol_rmsnorm_quant(chol_dtype dtype, int64_t rows, int64_t cols, int64_t group,
+                               const void *x, int64_t ldx,
+                               const void *residual, int64_t ldr,
+                               const void *w, float eps,
+                               void *q, int64_t ldq,
+                               float *scale, int64_t lds,
+                               void *h, int64_t ldh, void *stream);
+
+/*
+ * chol_rmsnorm_adjoint -- reverse-mode adjoint of chol_rmsnorm.  With
+ * s = (mean(h^2) + eps)^(-1/2) and g = adj w,
+ *     adjX = s (g - h s^2 mean(g h)) + adjH,      adjW (+)= sum over rows of adj h s.
+ *   h      [in]  the normalised rows (chol_rmsnorm's h, or its x without a
+ *          residual).  adjX is the gradient of h, so of x and of the residual.
+ *   adj    [in]  gradient of y; adjH [in] gradient that reaches h past the
+ *          norm, or NULL.
+ *   adjX   [out] device; may be h, adj or adjH itself.
+ *   adjW   [out] device fp32, cols elements; accumulate != 0 adds to it.  The
+ *          rows' terms are added in an order that depends on the sizes only.
+ *   workspace  at least chol_rmsnorm_adjoint_workspace_size bytes (4-byte
+ *          aligned; NULL allowed when it is 0).
+ */
+chol_status chol_rmsnorm_adjoint(chol_dtype dtype, int64_t rows, int64_t cols,
+                                 const void *h, int64_t ldh, const void *w,
+                                 const void *adj, int64_t lda,
+                                 const void *adjH, int64_t ldah, float eps,
+                                 void *adjX, int64_t ldax,
+                                 float *adjW, int accumulate,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace chol_rmsnorm_adjoint needs. */
+chol_status chol_rmsnorm_adjoint_workspace_size(chol_dtype dtype, int64_t rows, int64_t cols, size_t *bytes);
+
+/*
+ * chol_adamw -- one AdamW step over every tensor of a list, in one launch:
+ *     g' = grad_scale g,
+ *     m = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2,
+ *     p = p - lr weight_decay p - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps).
+ * The list (chol_adamw_list) is made once and used for every step:
+ *   dtype   CHOL_F32, CHOL_BF16 or CHOL_F16, of p and g.
+ *   bits    32: m and v are fp32.  8: m and sqrt(v) are e4m3 codes, the element
+ *           a code times its tile's scale; a tile is 256 elements of one tensor
+ *           (the last may be shorter).  Scales are powers of two that bring the
+ *           tile's largest element into [2^7, 2^8), but at least 2^-126.  A code is rounded up in
+ *           magnitude where 16 random bits and the dropped part carry; a nonzero
+ *           sqrt(v) is never stored as zero.  The random bits of the element at
+ *           position k of the list are those of (k + h(seed)) mod 2^32 under an integer
+ *           hash h, low half for m and high half for sqrt(v).
+ *   master  nonzero: the tensors have fp32 master weights, which are read and
+ *           updated, and p is written with their rounding; zero: p itself is.
+ * State and weight arithmetic is fp32, each product and sum rounded by itself.
+ *   chunks, table   what chol_adamw_list gave; the table lies in device memory
+ *           (8-byte aligned), copied there by the caller, and the tensors stay
+ *           where they are for as long as it is used.
+ *   grad_scale  device fp32[1] that every gradient is multiplied by (a clipping
+ *           factor, an inverse loss scale), or NULL for 1.
+ *   step    the number of this step, from 1; seed: its random sequence (bits 8).
+ *   Refused: beta1 or beta2 outside [0, 1), eps < 0, step < 1, values that are
+ *           not finite.
+ */
+chol_status chol_adamw(chol_dtype dtype, int bits, int master, int64_t chunks, const void *table,
+                       const float *grad_scale, double lr, double beta1, double beta2, double eps,
+                       double weight_decay, int64_t step, uint32_t seed, void *stream);
+
+/* One tensor of an AdamW list; every pointer is a device pointer, every array
+ * contiguous. */
+typedef struct {
+    void *p;             /* n weights */
+    const void *g;       /* n gradients, of p's type */
+    void *m, *v;         /* n states: fp32, or e4m3 codes */
+    float *master;       /* n fp32 weights; NULL in every tensor of a list without them */
+    float *m_scale;      /* ceil(n / 256) scales; not used for bits = 32 */
+    float *v_scale;
+    int64_t n;           /* 0 is skipped */
+    int64_t first;       /* position of element 0 in the random sequence (taken modulo 2^32) */
+} chol_adamw_tensor;
+
+/*
+ * chol_adamw_list -- the work list of chol_adamw, made on the host (calls no GPU
+ * function).  `tensors` is a host array.  Writes the number of chunks and the
+ * table's bytes, and, unless `table` is NULL, the table itself into host memory
+ * of table_bytes (fewer than needed: CHOL_ERR_WORKSPACE).  Arrays that are
+ * written may not share memory with any other array of the list.
+ */
+chol_status chol_adamw_list(chol_dtype dtype, int bits, int64_t count, const chol_adamw_tensor *tensors,
+                            void *table, size_t table_bytes, int64_t *chunks, size_t *bytes);
+
 /*
  * chol_wave_dot_fwd_adj -- diagnostic kernel for the reduction/broadcast
  * pattern the small-tile kernels rely on (Warp issue #1374, "adj_tile_dot is
@@ -561,7 +684,10 @@ typedef enum {
     CHOL_K_SOLVE_ADJOINT = 13,   /* the adj_L term of chol_potrs_adjoint*; flops: 4 n^2 nrhs per matrix */
     CHOL_K_RECURRENCE = 14,      /* chol_recurrence, whole calls; bytes: 3 * batch * len * dim * elem */
     CHOL_K_RECURRENCE_ADJOINT = 15, /* chol_recurrence_adjoint, whole calls; bytes: 5 * batch * len * dim * elem */
-    CHOL_K_COUNT = 16
+    CHOL_K_RMSNORM = 16,         /* chol_rmsnorm, chol_rmsnorm_quant; bytes of the arrays read and written */
+    CHOL_K_RMSNORM_ADJOINT = 17, /* chol_rmsnorm_adjoint, whole calls; bytes of the arrays read and written */
+    CHOL_K_ADAMW = 18,           /* chol_adamw; bytes moved (whole chunks counted) */
+    CHOL_K_COUNT = 19
 } chol_kernel_family;
 
 #define CHOL_PROFILE_ALL 0xffffffffu

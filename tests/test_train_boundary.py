@@ -103,3 +103,135 @@ def test_binding_refuses():
         dc.chol_recurrence(a, a, gate="tanh")
     with pytest.raises(ValueError):
         dc.chol_recurrence_adjoint(a, a, a[:, :2])
+
+
+# ------------------------------------------------------------------- norm ----
+
+def norm(dt=BF16, rows=10, cols=64, x=(P[0], 64), r=(P[1], 64), w=P[2], eps=1e-6, y=(P[3], 64), h=(P[4], 64)):
+    return lib.chol_rmsnorm(dt, rows, cols, *x, *r, w, eps, *y, *h, None)
+
+
+def quant(dt=BF16, rows=10, cols=64, group=32, x=(P[0], 64), r=(P[1], 64), w=P[2], eps=1e-6, q=(P[3], 64),
+          scale=(P[4], 2), h=(P[5], 64)):
+    return lib.chol_rmsnorm_quant(dt, rows, cols, group, *x, *r, w, eps, *q, *scale, *h, None)
+
+
+def norm_adjoint(dt=BF16, rows=2000, cols=64, h=(P[0], 64), w=P[1], adj=(P[2], 64), past=(P[3], 64), eps=1e-6,
+                 dx=(P[4], 64), dw=P[5], acc=0, ws=P[6], wbytes=1 << 40):
+    return lib.chol_rmsnorm_adjoint(dt, rows, cols, *h, w, *adj, *past, eps, *dx, dw, acc, ws, wbytes, None)
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(dt=F64), INVALID), (dict(rows=-1), INVALID), (dict(cols=-1), INVALID), (dict(rows=0), OK), (dict(cols=0), OK),
+    (dict(cols=16385), NOTSUP), (dict(rows=1 << 31), NOTSUP), (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
+    (dict(x=(None, 64)), INVALID), (dict(w=None), INVALID), (dict(y=(None, 64)), INVALID), (dict(h=(None, 64)), INVALID),
+    (dict(x=(P[0], 63)), INVALID), (dict(y=(P[3], 63)), INVALID), (dict(r=(P[1], -64)), INVALID),
+    (dict(y=(P[0] + 2, 64)), INVALID), (dict(y=(P[0], 65)), INVALID), (dict(y=(P[4], 64)), INVALID),
+    (dict(h=(P[2], 64)), INVALID), (dict(y=(P[2] - 64, 64)), INVALID), (dict(h=(P[1] + 2, 64)), INVALID),
+])
+def test_norm_refusals(change, expect):
+    assert norm(**change) == expect
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(group=16), INVALID), (dict(group=96), INVALID), (dict(group=512), INVALID), (dict(group=-32), INVALID),
+    (dict(rows=0), OK), (dict(q=(P[0], 64)), INVALID), (dict(scale=(P[4], 1)), INVALID), (dict(scale=(None, 2)), INVALID),
+    (dict(scale=(P[3], 2)), INVALID), (dict(q=(P[5], 64)), INVALID), (dict(scale=(P[1], 2)), INVALID),
+])
+def test_quant_refusals(change, expect):
+    assert quant(**change) == expect
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(dt=F64), INVALID), (dict(cols=16385), NOTSUP), (dict(cols=0), OK), (dict(eps=-1e-9), INVALID),
+    (dict(dw=None), INVALID), (dict(w=None), INVALID), (dict(h=(None, 64)), INVALID), (dict(adj=(None, 64)), INVALID),
+    (dict(dx=(None, 64)), INVALID), (dict(dx=(P[2] + 2, 64)), INVALID), (dict(dw=P[4]), INVALID), (dict(dw=P[0]), INVALID),
+    (dict(dw=P[1]), INVALID), (dict(dx=(P[1], 64)), INVALID),
+    (dict(ws=None, wbytes=0), WS), (dict(wbytes=100), WS), (dict(ws=P[6] + 2), INVALID), (dict(ws=P[4]), INVALID),
+    (dict(ws=P[2]), INVALID), (dict(ws=P[5]), INVALID), (dict(past=(P[3], 3)), INVALID),
+])
+def test_norm_adjoint_refusals(change, expect):
+    assert norm_adjoint(**change) == expect
+
+
+def test_norm_binding_refuses():
+    x, w = torch.zeros(3, 8), torch.ones(8)
+    with pytest.raises(ValueError):
+        dc.chol_rmsnorm(x, w)
+    with pytest.raises(ValueError):
+        dc.chol_rmsnorm(x, w[:7])
+    with pytest.raises(TypeError):
+        dc.chol_rmsnorm(x, w.half())
+    with pytest.raises(ValueError):
+        dc.chol_rmsnorm_quant(x, w, group=48)
+    with pytest.raises(ValueError):
+        dc.chol_rmsnorm_adjoint(x, w, x[:2])
+
+
+# ------------------------------------------------------------------ AdamW ----
+
+def adamw_list(dt=BF16, bits=8, table=None, room=0, **change):
+    items = (dc._train.AdamwTensor * 2)()
+    for i in range(2):
+        fields = dict(p=P[0], g=P[1], m=P[2], v=P[3], master=P[4], m_scale=P[5], v_scale=P[6], n=5000, first=0)
+        for k in fields:
+            if k not in ("n", "first"):
+                fields[k] += i << 20
+        if i == 1:
+            fields.update(change)
+        for k, x in fields.items():
+            setattr(items[i], k, x)
+    chunks, size = ctypes.c_int64(-1), ctypes.c_size_t(0)
+    s = lib.chol_adamw_list(dt, bits, 2, items, table, room, ctypes.byref(chunks), ctypes.byref(size))
+    return s, chunks.value, size.value
+
+
+def test_adamw_list():
+    s, chunks, size = adamw_list()
+    assert s == OK and chunks == 4 and size == 4 * 64
+    buf = ctypes.create_string_buffer(size)
+    at = ctypes.addressof(buf)
+    assert adamw_list(table=at, room=size - 1)[0] == WS
+    assert adamw_list(table=at, room=size)[0] == OK
+    words = (ctypes.c_uint64 * 32).from_buffer(buf)
+    assert words[0] == P[0] and words[8] == P[0] + 2 * 4096 and words[10] == P[2] + 4096 and words[13] == P[5] + 4 * 16
+    assert words[7] == 4096 and words[15] == 904 + (4096 << 32)
+    assert adamw_list(n=0)[:2] == (OK, 2)
+    assert adamw_list(g=P[1])[0] == OK             # a gradient that two tensors share is only read
+
+
+@pytest.mark.parametrize("change", [
+    dict(dt=F64), dict(bits=16), dict(n=-1), dict(p=None), dict(g=None), dict(m=None), dict(v=None), dict(m_scale=None),
+    dict(master=None), dict(p=P[0] + 1 + (1 << 20)), dict(master=P[4] + 2 + (1 << 20)), dict(p=P[0]), dict(p=P[0] + 9998),
+    dict(g=P[0] + 100), dict(m=P[2] + 4999), dict(v=P[2]), dict(m_scale=P[6]), dict(master=P[1] + 4),
+])
+def test_adamw_list_refusals(change):
+    assert adamw_list(**change)[0] == INVALID
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(dt=F64), INVALID), (dict(bits=4), INVALID), (dict(chunks=-1), INVALID), (dict(chunks=0), OK),
+    (dict(table=None), INVALID), (dict(table=P[0] + 4), INVALID), (dict(clip=P[1] + 2), INVALID),
+    (dict(beta1=1.0), INVALID), (dict(beta2=-0.1), INVALID), (dict(beta1=float("nan")), INVALID), (dict(eps=-1.0), INVALID),
+    (dict(lr=float("inf")), INVALID), (dict(wd=float("nan")), INVALID), (dict(step=0), INVALID),
+])
+def test_adamw_refusals(change, expect):
+    a = dict(dt=BF16, bits=8, master=1, chunks=4, table=P[0], clip=P[1], lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, wd=0.1,
+             step=1, seed=0, stream=None)
+    a.update(change)
+    assert lib.chol_adamw(*a.values()) == expect
+
+
+def test_adamw_binding_refuses():
+    t = [torch.zeros(8)]
+    with pytest.raises(ValueError):
+        dc.chol_adamw_list([], [], [], [])
+    with pytest.raises(ValueError):
+        dc.chol_adamw_list(t, t, t, t)                 # not on the GPU
+    with pytest.raises(TypeError):
+        dc.chol_adamw_list(t, t, [x.half() for x in t], t)
+    with pytest.raises(ValueError):
+        dc.chol_adamw_list(t, t, t, t, m_scale=t)
+    e = [torch.zeros(8, dtype=torch.uint8).view(torch.float8_e4m3fn)]
+    with pytest.raises(ValueError):
+        dc.chol_adamw_list(t, t, e, e)
