@@ -148,6 +148,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
                 h.set(i, k, h.at(i, k) * s * w.at(i, k));
         h.store((T *)a.y + row * a.ldy, t, cols);
     } else {
+        // s is common to the row: a code is h w / max |h w| * 448, which leaves s's
+        // rounding to the scale alone
         float y[NV][V];
         unsigned most[NV];
 #pragma unroll
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
             most[i] = 0;
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                y[i][k] = h.at(i, k) * s * w.at(i, k);
+                y[i][k] = h.at(i, k) * w.at(i, k);
                 most[i] = MaxBits::of(most[i], __float_as_uint(y[i][k]) & 0x7fffffffu);
             }
         }
@@ -177,14 +179,16 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * V;
-            const unsigned m = a.group ? most[i] : most[0];
+            const float m = __uint_as_float(a.group ? most[i] : most[0]), top = m * s;
             // one for a group of zeros (or with a NaN); not below the smallest
             // normal number, whose reciprocal still is one
-            const float sc = m == 0 || m > 0x7f800000u ? 1.f : fmaxf(__uint_as_float(m) * (1.f / E4M3_MAX), 0x1p-126f);
-            const float inv = __frcp_rn(sc);
+            const bool some = top > 0.f;
+            const float sc = some ? fmaxf(__fdiv_rn(top, E4M3_MAX), 0x1p-126f) : 1.f;
+            const bool plain = some && sc > 0x1p-126f && m > 0x1p-110f; // 448 / m is finite
+            const float pre = plain ? 1.f : s, inv = __fdiv_rn(plain ? E4M3_MAX : 1.f, plain ? m : sc);
 #pragma unroll
             for (int k = 0; k < V; ++k)
-                y[i][k] *= inv;
+                y[i][k] = y[i][k] * pre * inv;
             if (c < cols) {
                 store_e4m3<V>(q + c, y[i], cols - c);
                 if (a.group ? c % a.group == 0 : c == 0)
