@@ -1,14 +1,19 @@
 // The gated linear recurrence h_t = a_t h_{t-1} + b_t and its adjoint.
 //
 // Both are compositions of affine maps of one fp32 number a channel.  Forward,
-// step t maps x -> a_t x + b_t.  The adjoint runs from the last step to the
+// step t maps x -> a_t x + b_t.  The adjoint walks from the last step to the
 // first on mu_t = a_t lam_t with lam_t = adj_t + mu_{t+1}: step t maps
 // x -> a_t x + a_t adj_t, so a step needs its own gate only and the walk ends
 // with adj_h0 = mu_0.  A run of steps composes to x -> P x + Q.
 //
-// A sequence is cut into segments.  One kernel forms each segment's (P, Q); a
-// second joins those before a segment, which gives the state it starts from,
-// and walks the segment again, now writing.
+// One pass over memory: a lane holds R consecutive steps of one 32-bit word of
+// channels (two 16-bit ones, or an fp32 one) in registers, composes them, and
+// walks them again from registers once it knows the state before them.  Waves
+// of a workgroup lie along the steps (`waves`, fewer for short sequences) and
+// across channels, and exchange their (P, Q) through LDS.  Workgroups of one
+// channel group form a chain along the sequence: each publishes its own (P, Q),
+// looks back over those before it until it meets a known state, and publishes
+// the state after it.
 #include <algorithm>
 #include <type_traits>
 
@@ -19,115 +24,389 @@ namespace chol {
 
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int WAVE = 64, WAVES = 8, THREADS = WAVE * WAVES;
+constexpr int WINDOW = 4; // links of a chain read at once
 
-template <typename T> struct Rows {
-    T *p;
-    int64_t ld;
-    explicit __device__ Rows(const RecRows &r, int64_t b, int64_t c) : p((T *)r.p + b * r.stride + c), ld(r.ld) {}
-    __device__ __forceinline__ float at(int64_t t) const { return (float)p[t * ld]; }
-    __device__ __forceinline__ void put(int64_t t, float x) const { p[t * ld] = (T)x; }
+template <typename T> constexpr int word_channels = 4 / (int)sizeof(T);
+
+template <typename T> __device__ __forceinline__ float part(uint32_t w, int i)
+{
+    if constexpr (sizeof(T) == 4)
+        return __uint_as_float(w);
+    else
+        return (float)__builtin_bit_cast(T, (uint16_t)(w >> (16 * i)));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack(const float (&x)[word_channels<T>])
+{
+    if constexpr (sizeof(T) == 4) {
+        return __float_as_uint(x[0]);
+    } else {
+        vec<T, 2> v;
+        v[0] = (T)x[0];
+        v[1] = (T)x[1];
+        return __builtin_bit_cast(uint32_t, v);
+    }
+}
+template <typename T> __device__ __forceinline__ uint32_t load_word(const T *p)
+{
+    uint32_t w;
+    __builtin_memcpy(&w, p, 4);
+    return w;
+}
+template <typename T> __device__ __forceinline__ void store_word(T *p, uint32_t w) { __builtin_memcpy(p, &w, 4); }
+
+// the word's channels c .. c + V - 1 that lie below dim, else `none`'s
+template <typename T> __device__ __forceinline__ uint32_t load_part(const T *p, int64_t c, int64_t dim, uint32_t none)
+{
+    if constexpr (sizeof(T) == 4)
+        return c < dim ? __float_as_uint(*p) : none;
+    else
+        return (c < dim ? (uint32_t)__builtin_bit_cast(uint16_t, p[0]) : none & 0xffffu) |
+               (c + 1 < dim ? (uint32_t)__builtin_bit_cast(uint16_t, p[1]) << 16 : none & 0xffff0000u);
+}
+template <typename T> __device__ __forceinline__ void store_part(T *p, int64_t c, int64_t dim, uint32_t w)
+{
+#pragma unroll
+    for (int i = 0; i < word_channels<T>; ++i)
+        if (c + i < dim) {
+            if constexpr (sizeof(T) == 4)
+                p[i] = __uint_as_float(w);
+            else
+                p[i] = __builtin_bit_cast(T, (uint16_t)(w >> (16 * i)));
+        }
+}
+template <typename T> __device__ __forceinline__ uint32_t one_word()
+{
+    float x[word_channels<T>];
+    for (float &v : x)
+        v = 1.f;
+    return pack<T>(x);
+}
+
+// exp(x) from the hardware's 2^y: the product x log2(e) is carried in two
+// parts, or its rounding would grow with |x|.
+template <bool LOG> __device__ __forceinline__ float gate(float x)
+{
+    if constexpr (!LOG)
+        return x;
+    constexpr float L = 1.44269504088896340736f, L_LOW = 1.92596299112661746887e-8f, LN2 = 0.693147180559945309417f;
+    const float y = x * L, low = fmaf(x, L_LOW, fmaf(x, L, -y)), e = __builtin_amdgcn_exp2f(y);
+    // beyond +-128 the result is 0 or inf (and low may be NaN)
+    return fabsf(y) < 128.f ? fmaf(e * LN2, low, e) : e;
+}
+
+struct Plan {
+    int waves;          // of a workgroup along the steps; the others lie across channels
+    int steps;          // R
+    int chunks, groups; // workgroups along the steps, and across a batch element's channels
 };
 
-template <bool LOG> __device__ __forceinline__ float gate(float x) { return LOG ? expf(x) : x; }
+// Links of a chain: (P, Q) of a workgroup's steps in one 64-bit word a channel,
+// written and read whole, so that no flag or fence is needed.  The workspace is
+// filled with EMPTY first (P's NaN of all ones, which a published P never is).
+// A P of minus zero marks Q as the state itself (published Ps have no minus
+// zero).
+constexpr uint64_t EMPTY = ~(uint64_t)0;
+constexpr uint32_t KNOWN = 0x80000000u;
 
-// step s of the walk is row s (forward) or len - 1 - s (adjoint)
-template <bool ADJ> __device__ __forceinline__ int64_t row_of(int64_t s, int64_t len) { return ADJ ? len - 1 - s : s; }
-
-// (P, Q) of segment blockIdx.y of batch element blockIdx.z; ws[(z * segments + y) * dim + channel]
-template <typename T, bool LOG, bool ADJ>
-__global__ void __launch_bounds__(THREADS) k_rec_segment(RecArgs r, int64_t seg, float2 *ws)
+__device__ __forceinline__ void publish(uint64_t *p, uint32_t P, float Q)
 {
-    const int64_t c = (int64_t)blockIdx.x * THREADS + threadIdx.x, z = blockIdx.z;
-    if (c >= r.dim)
-        return;
-    const Rows<T> a(r.a, z, c), b(r.b, z, c);
-    const int64_t s0 = (int64_t)blockIdx.y * seg, s1 = min(s0 + seg, r.len);
-    float P = 1.f, Q = 0.f;
-    for (int64_t s = s0; s < s1; ++s) {
-        const int64_t t = row_of<ADJ>(s, r.len);
-        const float g = gate<LOG>(a.at(t)), x = b.at(t);
-        Q = ADJ ? g * (Q + x) : g * Q + x;
-        P *= g;
-    }
-    // the first segment's slot holds the state before and after it: the walk
-    // may then write the end over the start
-    if (blockIdx.y == 0) {
-        const float x = r.start ? r.start[z * r.dim + c] : 0.f;
-        Q = P * x + Q;
-        P = x;
-    }
-    ws[(z * gridDim.y + blockIdx.y) * r.dim + c] = make_float2(P, Q);
+    __hip_atomic_store(p, (uint64_t)P | (uint64_t)__float_as_uint(Q) << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t peek(const uint64_t *p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint32_t link_p(float P)
+{
+    return P != P ? 0x7fc00000u : P == 0.f ? 0u : __float_as_uint(P);
 }
 
-template <typename T, bool LOG, bool ADJ>
-__global__ void __launch_bounds__(THREADS) k_rec_walk(RecArgs r, int64_t seg, const float2 *ws)
+__global__ void __launch_bounds__(256) k_rec_clear(uint64_t *ws, int64_t links)
 {
-    const int64_t c = (int64_t)blockIdx.x * THREADS + threadIdx.x, z = blockIdx.z;
-    if (c >= r.dim)
-        return;
-    float x;
-    if (gridDim.y == 1) {
-        x = r.start ? r.start[z * r.dim + c] : 0.f;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i == 0)
+        ws[0] = 0; // tickets
+    else if (i <= links)
+        ws[i] = EMPTY;
+}
+
+template <typename T, bool LOG, bool ADJ, int R>
+__global__ void __launch_bounds__(THREADS) k_recurrence(RecArgs r, Plan p, uint64_t *ws)
+{
+    constexpr int V = word_channels<T>, SPAN = WAVE * V;
+    __shared__ float2 s_link[WAVES][SPAN];
+    __shared__ float s_in[WAVES][SPAN];
+    __shared__ unsigned s_ticket;
+    const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int jw = wave % p.waves, cw = wave / p.waves, across = WAVES / p.waves;
+    unsigned block = blockIdx.x;
+    if (p.chunks > 1) {
+        // chains advance in the order in which workgroups start: whatever a
+        // workgroup waits for has been started before it
+        if (threadIdx.x == 0)
+            s_ticket = atomicAdd((unsigned *)ws, 1u);
+        __syncthreads();
+        block = __builtin_amdgcn_readfirstlane(s_ticket);
+    }
+    const unsigned chains = (unsigned)(r.batch * p.groups);
+    const unsigned chunk = block / chains, chain = block % chains;
+    const int64_t z = chain / p.groups;
+    const int64_t c0 = ((int64_t)(chain % p.groups) * across + cw) * SPAN, c = c0 + lane * V;
+    const int64_t s0 = ((int64_t)chunk * p.waves + jw) * R;
+    // walk step s is row s, or counted from the end
+    const auto row = [&](int64_t s) { return ADJ ? r.len - 1 - s : s; };
+    const T *pa = (const T *)r.a.p + z * r.a.stride + c0, *pb = (const T *)r.b.p + z * r.b.stride + c0;
+    const T *ph = ADJ ? (const T *)r.h.p + z * r.h.stride + c0 : nullptr;
+    const bool whole = c0 + SPAN <= r.dim && s0 + R + (ADJ ? 1 : 0) <= r.len;
+
+    uint32_t a[R], b[R], h[ADJ ? R : 1]; // h: the state before the step
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            a[i] = load_word(pa + row(s0 + i) * r.a.ld + lane * V);
+            b[i] = load_word(pb + row(s0 + i) * r.b.ld + lane * V);
+        }
+        if constexpr (ADJ)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                h[i] = load_word(ph + row(s0 + i + 1) * r.h.ld + lane * V);
     } else {
-        const float2 first = ws[z * gridDim.y * r.dim + c];
-        x = blockIdx.y ? first.y : first.x;
-        for (int64_t y = 1; y < blockIdx.y; ++y) {
-            const float2 pq = ws[(z * gridDim.y + y) * r.dim + c];
-            x = pq.x * x + pq.y;
+        // steps past the end and channels past dim leave the state as it is
+        const uint32_t open = LOG ? 0u : one_word<T>();
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const bool in = s0 + i < r.len;
+            a[i] = in ? load_part(pa + row(s0 + i) * r.a.ld + lane * V, c, r.dim, open) : open;
+            b[i] = in ? load_part(pb + row(s0 + i) * r.b.ld + lane * V, c, r.dim, 0u) : 0u;
+            if constexpr (ADJ)
+                h[i] = s0 + i + 1 < r.len ? load_part(ph + row(s0 + i + 1) * r.h.ld + lane * V, c, r.dim, 0u) : 0u;
         }
     }
-    const Rows<T> a(r.a, z, c), b(r.b, z, c), out(r.out, z, c);
-    const int64_t s0 = (int64_t)blockIdx.y * seg, s1 = min(s0 + seg, r.len);
-    for (int64_t s = s0; s < s1; ++s) {
-        const int64_t t = row_of<ADJ>(s, r.len);
-        const float g = gate<LOG>(a.at(t));
-        if constexpr (ADJ) {
-            const float lam = b.at(t) + x;
-            const float before = t > 0 ? Rows<T>(r.h, z, c).at(t - 1) : r.h0 ? r.h0[z * r.dim + c] : 0.f;
-            x = g * lam;
-            Rows<T>(r.adj_a, z, c).put(t, before * (LOG ? x : lam));
-            out.put(t, lam);
-        } else {
-            x = g * x + b.at(t);
-            out.put(t, x);
+    const auto state = [&](const float *x, int v) { return x && c + v < r.dim ? x[z * r.dim + c + v] : 0.f; };
+
+    float x[V];
+    if (p.waves * p.chunks == 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            x[v] = state(r.start, v);
+    } else {
+        float P[V], Q[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            P[v] = 1.f, Q[v] = 0.f;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float g = gate<LOG>(part<T>(a[i], v)), y = part<T>(b[i], v);
+                Q[v] = ADJ ? g * (Q[v] + y) : fmaf(g, Q[v], y);
+                P[v] *= g;
+            }
+            s_link[wave][lane * V + v] = make_float2(P[v], Q[v]);
+        }
+        __syncthreads();
+        if (jw == 0) {
+            for (int k = 1; k < p.waves; ++k)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float2 n = s_link[wave + k][lane * V + v];
+                    Q[v] = fmaf(n.x, Q[v], n.y);
+                    P[v] *= n.x;
+                }
+            if (p.chunks > 1) {
+                const int64_t stride = (int64_t)across * SPAN;
+                uint64_t *link = ws + 1 + ((int64_t)chain * p.chunks + chunk) * stride + cw * SPAN + lane * V;
+                if (chunk == 0) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        x[v] = state(r.start, v);
+                } else {
+                    float bp[V], bq[V]; // what lies between the state looked for and this workgroup
+                    bool known[V];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        publish(link + v, link_p(P[v]), Q[v]);
+                        bp[v] = 1.f, bq[v] = 0.f;
+                        known[v] = false;
+                    }
+                    // link 0 of a chain is a known state, so the walk back ends there at the latest
+                    for (unsigned at = chunk; at > 0;) {
+                        const int n = at < WINDOW ? (int)at : WINDOW;
+                        uint64_t w[WINDOW][V];
+#pragma unroll
+                        for (int k = 0; k < WINDOW; ++k)
+#pragma unroll
+                            for (int v = 0; v < V; ++v)
+                                if (k < n)
+                                    w[k][v] = peek(link - (int64_t)(chunk - at + 1 + k) * stride + v);
+#pragma unroll
+                        for (int k = 0; k < WINDOW; ++k) {
+                            if (k >= n)
+                                continue;
+#pragma unroll
+                            for (int v = 0; v < V; ++v) {
+                                while ((uint32_t)w[k][v] == (uint32_t)EMPTY) {
+                                    __builtin_amdgcn_s_sleep(1);
+                                    w[k][v] = peek(link - (int64_t)(chunk - at + 1 + k) * stride + v);
+                                }
+                                const float q = __uint_as_float((uint32_t)(w[k][v] >> 32));
+                                if (!known[v]) {
+                                    bq[v] = fmaf(bp[v], q, bq[v]);
+                                    bp[v] *= __uint_as_float((uint32_t)w[k][v]);
+                                    known[v] = (uint32_t)w[k][v] == KNOWN;
+                                }
+                            }
+                        }
+                        bool all = true;
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            all = all && known[v];
+                        if (__all(all))
+                            break;
+                        at -= n;
+                    }
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        x[v] = bq[v];
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    publish(link + v, KNOWN, fmaf(P[v], x[v], Q[v]));
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    x[v] = state(r.start, v);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                s_in[cw][lane * V + v] = x[v];
+        }
+        __syncthreads();
+        if (jw > 0) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                x[v] = s_in[cw][lane * V + v];
+            for (int k = 0; k < jw; ++k)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float2 n = s_link[wave - jw + k][lane * V + v];
+                    x[v] = fmaf(n.x, x[v], n.y);
+                }
         }
     }
-    if (r.end && blockIdx.y == gridDim.y - 1)
-        r.end[z * r.dim + c] = x;
+
+    // the words are unpacked again: values kept from the first walk would take
+    // twice the registers, and half the waves
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        asm volatile("" : "+v"(a[i]), "+v"(b[i]));
+
+    T *po = (T *)r.out.p + z * r.out.stride + c0;
+    T *pd = ADJ ? (T *)r.adj_a.p + z * r.adj_a.stride + c0 : nullptr;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        float out[V], da[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float g = gate<LOG>(part<T>(a[i], v)), y = part<T>(b[i], v);
+            if constexpr (ADJ) {
+                const float lam = y + x[v];
+                float before = part<T>(h[i], v);
+                if (!whole && s0 + i + 1 == r.len)
+                    before = state(r.h0, v);
+                x[v] = g * lam;
+                da[v] = before * (LOG ? x[v] : lam);
+                out[v] = lam;
+            } else {
+                x[v] = fmaf(g, x[v], y);
+                out[v] = x[v];
+            }
+        }
+        T *o = po + row(s0 + i) * r.out.ld + lane * V, *d = ADJ ? pd + row(s0 + i) * r.adj_a.ld + lane * V : nullptr;
+        if (whole) {
+            store_word(o, pack<T>(out));
+            if constexpr (ADJ)
+                store_word(d, pack<T>(da));
+        } else if (s0 + i < r.len) {
+            store_part(o, c, r.dim, pack<T>(out));
+            if constexpr (ADJ)
+                store_part(d, c, r.dim, pack<T>(da));
+        }
+    }
+    if (chunk == (unsigned)p.chunks - 1 && jw == p.waves - 1)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (c + v < r.dim)
+                r.end[z * r.dim + c + v] = x[v];
 }
 
-// Steps of a segment: whole sequences where channels alone give 2^17 threads
-// (two waves a SIMD on 256 CUs), else as many segments as bring them there.
-int64_t segment_of(int64_t batch, int64_t len, int64_t dim)
+int ceil_pow2(int64_t x, int most)
 {
-    const int64_t threads = batch * ((dim + THREADS - 1) / THREADS) * THREADS;
-    const int64_t want = std::max<int64_t>(1, ((int64_t)1 << 17) / threads);
-    return std::max<int64_t>(16, (len + want - 1) / want);
+    int p = 1;
+    while (p < x && p < most)
+        p *= 2;
+    return p;
 }
 
-template <typename T, bool LOG, bool ADJ> chol_status run(const RecArgs &r, void *ws, hipStream_t st)
+constexpr int SHORT = 8, LONG = 32, LONG_ADJOINT = 16; // R
+
+Plan plan_of(chol_dtype dt, bool adjoint, int64_t batch, int64_t len, int64_t dim)
 {
-    const int64_t seg = segment_of(r.batch, r.len, r.dim);
-    if (r.batch > 65535)
-        return CHOL_ERR_NOT_SUPPORTED;
-    const int64_t parts = std::max<int64_t>(1, (r.len + seg - 1) / seg);
-    const dim3 grid((unsigned)((r.dim + THREADS - 1) / THREADS), (unsigned)parts, (unsigned)r.batch);
-    if (parts > 1) {
-        hipLaunchKernelGGL((k_rec_segment<T, LOG, ADJ>), grid, dim3(THREADS), 0, st, r, seg, (float2 *)ws);
+    const int64_t span = WAVE * (4 / (int64_t)lowp_size(dt));
+    const auto with = [&](int steps) {
+        Plan p;
+        p.steps = steps;
+        p.waves = ceil_pow2((len + steps - 1) / steps, WAVES);
+        p.chunks = (int)std::max<int64_t>(1, (len + p.waves * steps - 1) / (p.waves * steps));
+        const int64_t width = span * (WAVES / p.waves);
+        p.groups = (int)((dim + width - 1) / width);
+        return p;
+    };
+    if (len <= 1)
+        return with(1);
+    const Plan p = with(adjoint ? LONG_ADJOINT : LONG);
+    return (int64_t)p.chunks * p.groups * batch >= 512 ? p : with(SHORT);
+}
+
+int64_t links_of(chol_dtype dt, const Plan &p, int64_t batch)
+{
+    return p.chunks > 1 ? batch * p.groups * p.chunks * WAVE * (4 / (int64_t)lowp_size(dt)) * (WAVES / p.waves) : 0;
+}
+
+template <typename T, bool LOG, bool ADJ> chol_status run(chol_dtype dt, const RecArgs &r, void *ws, hipStream_t st)
+{
+    const Plan p = plan_of(dt, ADJ, r.batch, r.len, r.dim);
+    if (p.chunks > 1) {
+        const int64_t links = links_of(dt, p, r.batch);
+        hipLaunchKernelGGL(k_rec_clear, dim3((unsigned)((links + 1 + 255) / 256)), dim3(256), 0, st, (uint64_t *)ws, links);
         CHOL_LAUNCH_CHECK();
     }
-    hipLaunchKernelGGL((k_rec_walk<T, LOG, ADJ>), grid, dim3(THREADS), 0, st, r, seg, (const float2 *)ws);
+    const dim3 grid((unsigned)(r.batch * p.groups * p.chunks));
+    constexpr int L = ADJ ? LONG_ADJOINT : LONG;
+    if (p.steps == 1)
+        hipLaunchKernelGGL((k_recurrence<T, LOG, ADJ, 1>), grid, dim3(THREADS), 0, st, r, p, (uint64_t *)ws);
+    else if (p.steps == SHORT)
+        hipLaunchKernelGGL((k_recurrence<T, LOG, ADJ, SHORT>), grid, dim3(THREADS), 0, st, r, p, (uint64_t *)ws);
+    else
+        hipLaunchKernelGGL((k_recurrence<T, LOG, ADJ, L>), grid, dim3(THREADS), 0, st, r, p, (uint64_t *)ws);
     CHOL_LAUNCH_CHECK();
     return CHOL_OK;
 }
 
 } // namespace
 
-size_t recurrence_workspace(int64_t batch, int64_t len, int64_t dim)
+// bytes, or -1 where the workgroups are more than a grid holds
+int64_t recurrence_workspace(chol_dtype dt, int64_t batch, int64_t len, int64_t dim)
 {
-    const int64_t seg = segment_of(batch, len, dim), parts = (len + seg - 1) / seg;
-    return parts > 1 ? (size_t)(batch * parts * dim) * sizeof(float2) : 0;
+    int64_t bytes = 0;
+    for (const bool adjoint : {false, true}) {
+        const Plan p = plan_of(dt, adjoint, batch, len, dim);
+        if ((double)batch * p.groups * p.chunks > 2147483647.0)
+            return -1;
+        const int64_t links = links_of(dt, p, batch);
+        if (links)
+            bytes = std::max(bytes, (links + 1) * (int64_t)sizeof(uint64_t));
+    }
+    return bytes;
 }
 
 chol_status recurrence(chol_dtype dt, bool log_gate, bool adjoint, const RecArgs &r, void *ws, hipStream_t st)
@@ -135,8 +414,8 @@ chol_status recurrence(chol_dtype dt, bool log_gate, bool adjoint, const RecArgs
     return with_lowp(dt, [&](auto *t) {
         typedef std::remove_pointer_t<decltype(t)> T;
         if (adjoint)
-            return log_gate ? run<T, true, true>(r, ws, st) : run<T, false, true>(r, ws, st);
-        return log_gate ? run<T, true, false>(r, ws, st) : run<T, false, false>(r, ws, st);
+            return log_gate ? run<T, true, true>(dt, r, ws, st) : run<T, false, true>(dt, r, ws, st);
+        return log_gate ? run<T, true, false>(dt, r, ws, st) : run<T, false, false>(dt, r, ws, st);
     });
 }
 

@@ -24,7 +24,7 @@ struct RecArgs {
     float *end;           // state it ends with: forward hlast, adjoint adj_h0
 };
 
-size_t recurrence_workspace(int64_t batch, int64_t len, int64_t dim);
+int64_t recurrence_workspace(chol_dtype dt, int64_t batch, int64_t len, int64_t dim);
 chol_status recurrence(chol_dtype dt, bool log_gate, bool adjoint, const RecArgs &args, void *ws, hipStream_t st);
 
 } // namespace chol

@@ -41,7 +41,10 @@ chol_status chol_recurrence_workspace_size(chol_dtype dt, int64_t batch, int64_t
         return CHOL_OK;
     if (batch > INT32_MAX || len > INT32_MAX || dim > INT32_MAX || batch * dim > INT32_MAX)
         return CHOL_ERR_NOT_SUPPORTED;
-    *bytes = recurrence_workspace(batch, len, dim);
+    const int64_t need = recurrence_workspace(dt, batch, len, dim);
+    if (need < 0)
+        return CHOL_ERR_NOT_SUPPORTED;
+    *bytes = (size_t)need;
     return CHOL_OK;
 }
 
