@@ -11,9 +11,11 @@
 // walks them again from registers once it knows the state before them.  Waves
 // of a workgroup lie along the steps (`waves`, fewer for short sequences) and
 // across channels, and exchange their (P, Q) through LDS.  Workgroups of one
-// channel group form a chain along the sequence: each publishes its own (P, Q),
-// looks back over those before it until it meets a known state, and publishes
-// the state after it.
+// channel group form a chain along the sequence, cut into groups of LINKS: a
+// workgroup composes what those before it in its group published, and applies
+// that to the state its group starts from, which the last workgroup of the group
+// before published.  So the chain waits once a group, every sum is formed in
+// one order whatever the workgroups' timing, and equal calls give equal bits.
 #include <algorithm>
 #include <type_traits>
 
@@ -25,7 +27,7 @@ namespace chol {
 namespace {
 
 constexpr int WAVE = 64, WAVES = 8, THREADS = WAVE * WAVES;
-constexpr int WINDOW = 4; // links of a chain read at once
+constexpr int LINKS = 16, WINDOW = 4; // workgroups of a chain's group; words read at once
 
 template <typename T> constexpr int word_channels = 4 / (int)sizeof(T);
 
@@ -101,25 +103,29 @@ struct Plan {
     int chunks, groups; // workgroups along the steps, and across a batch element's channels
 };
 
-// Links of a chain: (P, Q) of a workgroup's steps in one 64-bit word a channel,
-// written and read whole, so that no flag or fence is needed.  The workspace is
-// filled with EMPTY first (P's NaN of all ones, which a published P never is).
-// A P of minus zero marks Q as the state itself (published Ps have no minus
-// zero).
+// What a workgroup publishes, one 64-bit word a channel, written once and read
+// whole, so that no flag or fence is needed: the (P, Q) of its steps, or, from
+// the last of a group, the state after it in Q.  The workspace is filled with
+// EMPTY first (P's NaN of all ones, which a published P never is).
 constexpr uint64_t EMPTY = ~(uint64_t)0;
-constexpr uint32_t KNOWN = 0x80000000u;
 
-__device__ __forceinline__ void publish(uint64_t *p, uint32_t P, float Q)
+__device__ __forceinline__ void publish(uint64_t *p, float P, float Q)
 {
-    __hip_atomic_store(p, (uint64_t)P | (uint64_t)__float_as_uint(Q) << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t bits = P != P ? 0x7fc00000u : __float_as_uint(P);
+    __hip_atomic_store(p, (uint64_t)bits | (uint64_t)__float_as_uint(Q) << 32, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ uint64_t peek(const uint64_t *p)
 {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ uint32_t link_p(float P)
+__device__ __forceinline__ float2 arrived(const uint64_t *p, uint64_t w)
 {
-    return P != P ? 0x7fc00000u : P == 0.f ? 0u : __float_as_uint(P);
+    while ((uint32_t)w == (uint32_t)EMPTY) {
+        __builtin_amdgcn_s_sleep(1);
+        w = peek(p);
+    }
+    return make_float2(__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32)));
 }
 
 __global__ void __launch_bounds__(256) k_rec_clear(uint64_t *ws, int64_t links)
@@ -214,63 +220,46 @@ __global__ void __launch_bounds__(THREADS) k_recurrence(RecArgs r, Plan p, uint6
                 }
             if (p.chunks > 1) {
                 const int64_t stride = (int64_t)across * SPAN;
-                uint64_t *link = ws + 1 + ((int64_t)chain * p.chunks + chunk) * stride + cw * SPAN + lane * V;
-                if (chunk == 0) {
+                uint64_t *const links = ws + 1 + (int64_t)chain * p.chunks * stride + cw * SPAN + lane * V;
+                const auto link = [&](unsigned at, int v) { return links + (int64_t)at * stride + v; };
+                const unsigned first = chunk / LINKS * LINKS;
+                const bool last = chunk % LINKS == LINKS - 1, read = chunk + 1 < (unsigned)p.chunks;
+                if (!last && read)
 #pragma unroll
                     for (int v = 0; v < V; ++v)
-                        x[v] = state(r.start, v);
-                } else {
-                    float bp[V], bq[V]; // what lies between the state looked for and this workgroup
-                    bool known[V];
+                        publish(link(chunk, v), P[v], Q[v]);
+                float bp[V], bq[V]; // of the group's workgroups before this one
+                uint64_t base[V];
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        publish(link + v, link_p(P[v]), Q[v]);
-                        bp[v] = 1.f, bq[v] = 0.f;
-                        known[v] = false;
-                    }
-                    // link 0 of a chain is a known state, so the walk back ends there at the latest
-                    for (unsigned at = chunk; at > 0;) {
-                        const int n = at < WINDOW ? (int)at : WINDOW;
-                        uint64_t w[WINDOW][V];
+                for (int v = 0; v < V; ++v) {
+                    bp[v] = 1.f, bq[v] = 0.f;
+                    base[v] = first ? peek(link(first - 1, v)) : 0;
+                }
+                for (unsigned at = first; at < chunk; at += WINDOW) {
+                    uint64_t w[WINDOW][V];
 #pragma unroll
-                        for (int k = 0; k < WINDOW; ++k)
-#pragma unroll
-                            for (int v = 0; v < V; ++v)
-                                if (k < n)
-                                    w[k][v] = peek(link - (int64_t)(chunk - at + 1 + k) * stride + v);
-#pragma unroll
-                        for (int k = 0; k < WINDOW; ++k) {
-                            if (k >= n)
-                                continue;
-#pragma unroll
-                            for (int v = 0; v < V; ++v) {
-                                while ((uint32_t)w[k][v] == (uint32_t)EMPTY) {
-                                    __builtin_amdgcn_s_sleep(1);
-                                    w[k][v] = peek(link - (int64_t)(chunk - at + 1 + k) * stride + v);
-                                }
-                                const float q = __uint_as_float((uint32_t)(w[k][v] >> 32));
-                                if (!known[v]) {
-                                    bq[v] = fmaf(bp[v], q, bq[v]);
-                                    bp[v] *= __uint_as_float((uint32_t)w[k][v]);
-                                    known[v] = (uint32_t)w[k][v] == KNOWN;
-                                }
-                            }
-                        }
-                        bool all = true;
+                    for (int k = 0; k < WINDOW; ++k)
 #pragma unroll
                         for (int v = 0; v < V; ++v)
-                            all = all && known[v];
-                        if (__all(all))
-                            break;
-                        at -= n;
-                    }
+                            if (at + k < chunk)
+                                w[k][v] = peek(link(at + k, v));
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        x[v] = bq[v];
+                    for (int k = 0; k < WINDOW; ++k)
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            if (at + k < chunk) {
+                                const float2 n = arrived(link(at + k, v), w[k][v]);
+                                bq[v] = fmaf(n.x, bq[v], n.y);
+                                bp[v] *= n.x;
+                            }
                 }
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    publish(link + v, KNOWN, fmaf(P[v], x[v], Q[v]));
+                for (int v = 0; v < V; ++v) {
+                    const float from = first ? arrived(link(first - 1, v), base[v]).y : state(r.start, v);
+                    x[v] = chunk == first ? from : fmaf(bp[v], from, bq[v]);
+                    if (last && read)
+                        publish(link(chunk, v), 0.f, fmaf(P[v], x[v], Q[v]));
+                }
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
@@ -394,13 +383,13 @@ template <typename T, bool LOG, bool ADJ> chol_status run(chol_dtype dt, const R
 
 } // namespace
 
-// bytes, or -1 where the workgroups are more than a grid holds
+// bytes, or -1 where the threads are more than a grid holds
 int64_t recurrence_workspace(chol_dtype dt, int64_t batch, int64_t len, int64_t dim)
 {
     int64_t bytes = 0;
     for (const bool adjoint : {false, true}) {
         const Plan p = plan_of(dt, adjoint, batch, len, dim);
-        if ((double)batch * p.groups * p.chunks > 2147483647.0)
+        if ((double)batch * p.groups * p.chunks * THREADS > 4294967295.0)
             return -1;
         const int64_t links = links_of(dt, p, batch);
         if (links)

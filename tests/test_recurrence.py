@@ -200,3 +200,17 @@ def test_captured_into_a_graph():
         torch.cuda.synchronize()
         for x, y in zip((gh, gl, *gg), (*want, *grads)):
             assert torch.equal(x, y), k
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_equal_calls_give_equal_bits(dtype):
+    """Whatever order the workgroups of a long sequence finish in."""
+    import differentiable_cholesky_amd as dc
+    a, b, adj, h0, adj_last = make(2, 20000, 260, dtype, "log", True, seed=11)
+    h, last = dc.chol_recurrence(a, b, h0=h0, gate="log")
+    grads = dc.chol_recurrence_adjoint(a, h, adj, h0=h0, adjHlast=adj_last, gate="log")
+    for k in range(20):
+        again = dc.chol_recurrence(a, b, h0=h0, gate="log")
+        assert torch.equal(again[0], h) and torch.equal(again[1], last), k
+        for x, y in zip(dc.chol_recurrence_adjoint(a, h, adj, h0=h0, adjHlast=adj_last, gate="log"), grads):
+            assert torch.equal(x, y), k

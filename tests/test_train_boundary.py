@@ -41,6 +41,7 @@ def test_recurrence_workspace_size():
     assert need(F64, 1, 10, 10)[0] == INVALID
     assert need(F32, -1, 10, 10)[0] == INVALID
     assert need(F32, 1 << 20, 10, 1 << 20)[0] == NOTSUP
+    assert need(F32, 1 << 24, 1, 1)[0] == NOTSUP              # more threads than a grid holds
     assert lib.chol_recurrence_workspace_size(F32, 1, 1, 1, None) == INVALID
 
 
