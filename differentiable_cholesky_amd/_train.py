@@ -157,7 +157,7 @@ def chol_recurrence(a, b, h0=None, hlast=None, h=None, gate: str = "linear", wor
     batch, length, dim = a.shape
     with _on(a, stream):
         if h is None:
-            h = torch.empty((batch, length, dim), dtype=a.dtype, device=a.device)
+            h = torch.empty_like(a)
         else:
             _same(h, "h", a)
         if hlast is None:
@@ -185,11 +185,11 @@ def chol_recurrence_adjoint(a, h, adjH, h0=None, adjHlast=None, adjA=None, adjB=
     batch, length, dim = a.shape
     with _on(a, stream):
         if adjA is None:
-            adjA = torch.empty((batch, length, dim), dtype=a.dtype, device=a.device)
+            adjA = torch.empty_like(a)
         else:
             _same(adjA, "adjA", a)
         if adjB is None:
-            adjB = torch.empty((batch, length, dim), dtype=a.dtype, device=a.device)
+            adjB = torch.empty_like(a)
         else:
             _same(adjB, "adjB", a)
         if adjH0 is None:
@@ -242,7 +242,7 @@ def chol_rmsnorm(x, w, residual=None, eps: float = 1e-6, y=None, h=None, stream=
     with _on(x, stream):
         px, ldx = _rows(x, "x")
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            y = torch.empty_like(x)
         else:
             _same(y, "y", x)
         py, ldy = _rows(y, "y")
@@ -254,7 +254,7 @@ def chol_rmsnorm(x, w, residual=None, eps: float = 1e-6, y=None, h=None, stream=
             _same(residual, "residual", x)
             pr, ldr = _rows(residual, "residual")
             if h is None:
-                h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+                h = torch.empty_like(x)
             else:
                 _same(h, "h", x)
             ph, ldh = _rows(h, "h")
@@ -276,7 +276,7 @@ def chol_rmsnorm_quant(x, w, residual=None, group: int = 0, eps: float = 1e-6, q
     with _on(x, stream):
         px, ldx = _rows(x, "x")
         if q is None:
-            q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+            q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         else:
             _same(q, "q", x, dtype=torch.float8_e4m3fn)
         if scale is None:
@@ -293,7 +293,7 @@ def chol_rmsnorm_quant(x, w, residual=None, group: int = 0, eps: float = 1e-6, q
             _same(residual, "residual", x)
             pr, ldr = _rows(residual, "residual")
             if h is None:
-                h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+                h = torch.empty_like(x)
             else:
                 _same(h, "h", x)
             ph, ldh = _rows(h, "h")
@@ -318,7 +318,7 @@ def chol_rmsnorm_adjoint(h, w, adj, adjH=None, eps: float = 1e-6, adjX=None, adj
     _same(adj, "adj", h)
     with _on(h, stream):
         if adjX is None:
-            adjX = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+            adjX = torch.empty_like(h)
         else:
             _same(adjX, "adjX", h)
         if adjW is None:

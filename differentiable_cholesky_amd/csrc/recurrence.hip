@@ -27,7 +27,7 @@ namespace chol {
 namespace {
 
 constexpr int WAVE = 64, WAVES = 8, THREADS = WAVE * WAVES;
-constexpr int LINKS = 16, WINDOW = 4; // workgroups of a chain's group; words read at once
+constexpr int LINKS = 8, WINDOW = 4; // workgroups of a chain's group; words read at once
 
 template <typename T> constexpr int word_channels = 4 / (int)sizeof(T);
 
@@ -49,13 +49,18 @@ template <typename T> __device__ __forceinline__ uint32_t pack(const float (&x)[
         return __builtin_bit_cast(uint32_t, v);
     }
 }
+// Stores leave the caches to the loads: 8 x 4096 x 2048 bf16 forward 93 -> 72 us.
+// Loads that do so too lose where rows share cache lines (4 x 4095 x 1999 bf16
+// 68 -> 91 us) and gain 5% at most where they do not.
+typedef uint32_t any_word __attribute__((aligned(2)));
 template <typename T> __device__ __forceinline__ uint32_t load_word(const T *p)
 {
-    uint32_t w;
-    __builtin_memcpy(&w, p, 4);
-    return w;
+    return *(const any_word *)p;
 }
-template <typename T> __device__ __forceinline__ void store_word(T *p, uint32_t w) { __builtin_memcpy(p, &w, 4); }
+template <typename T> __device__ __forceinline__ void store_word(T *p, uint32_t w)
+{
+    __builtin_nontemporal_store(w, (any_word *)p);
+}
 
 // the word's channels c .. c + V - 1 that lie below dim, else `none`'s
 template <typename T> __device__ __forceinline__ uint32_t load_part(const T *p, int64_t c, int64_t dim, uint32_t none)
@@ -85,14 +90,19 @@ template <typename T> __device__ __forceinline__ uint32_t one_word()
     return pack<T>(x);
 }
 
-// exp(x) from the hardware's 2^y: the product x log2(e) is carried in two
-// parts, or its rounding would grow with |x|.
-template <bool LOG> __device__ __forceinline__ float gate(float x)
+// exp(x) from the hardware's 2^y.  Rounding y = x log2(e) changes the result by
+// up to |x| 2^-24 of itself.  For an fp32 x the product is carried in two parts;
+// a 16-bit x is itself off by |x| 2^-9 (2^-12 in fp16), so one part does: the
+// adjoint of 1 x 65536 x 2048 bf16 298 -> 272 us.
+template <typename T, bool LOG> __device__ __forceinline__ float gate(float x)
 {
+    constexpr float L = 1.44269504088896340736f, L_LOW = 1.92596299112661746887e-8f, LN2 = 0.693147180559945309417f;
     if constexpr (!LOG)
         return x;
-    constexpr float L = 1.44269504088896340736f, L_LOW = 1.92596299112661746887e-8f, LN2 = 0.693147180559945309417f;
-    const float y = x * L, low = fmaf(x, L_LOW, fmaf(x, L, -y)), e = __builtin_amdgcn_exp2f(y);
+    const float y = x * L, e = __builtin_amdgcn_exp2f(y);
+    if constexpr (sizeof(T) == 2)
+        return e;
+    const float low = fmaf(x, L_LOW, fmaf(x, L, -y));
     // beyond +-128 the result is 0 or inf (and low may be NaN)
     return fabsf(y) < 128.f ? fmaf(e * LN2, low, e) : e;
 }
@@ -203,7 +213,7 @@ __global__ void __launch_bounds__(THREADS) k_recurrence(RecArgs r, Plan p, uint6
             P[v] = 1.f, Q[v] = 0.f;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const float g = gate<LOG>(part<T>(a[i], v)), y = part<T>(b[i], v);
+                const float g = gate<T, LOG>(part<T>(a[i], v)), y = part<T>(b[i], v);
                 Q[v] = ADJ ? g * (Q[v] + y) : fmaf(g, Q[v], y);
                 P[v] *= g;
             }
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(THREADS) k_recurrence(RecArgs r, Plan p, uint6
         float out[V], da[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float g = gate<LOG>(part<T>(a[i], v)), y = part<T>(b[i], v);
+            const float g = gate<T, LOG>(part<T>(a[i], v)), y = part<T>(b[i], v);
             if constexpr (ADJ) {
                 const float lam = y + x[v];
                 float before = part<T>(h[i], v);
@@ -336,7 +346,7 @@ int ceil_pow2(int64_t x, int most)
     return p;
 }
 
-constexpr int SHORT = 8, LONG = 32, LONG_ADJOINT = 16; // R
+constexpr int SHORT = 8, LONG = 32, LONG_ADJOINT = 20; // R
 
 Plan plan_of(chol_dtype dt, bool adjoint, int64_t batch, int64_t len, int64_t dim)
 {
@@ -350,10 +360,12 @@ Plan plan_of(chol_dtype dt, bool adjoint, int64_t batch, int64_t len, int64_t di
         p.groups = (int)((dim + width - 1) / width);
         return p;
     };
-    if (len <= 1)
-        return with(1);
-    const Plan p = with(adjoint ? LONG_ADJOINT : LONG);
-    return (int64_t)p.chunks * p.groups * batch >= 512 ? p : with(SHORT);
+    // More steps a lane mean fewer links for the same bytes (1 x 65536 x 128 bf16
+    // forward 30 us with 32 steps, 92 with 8), up to what leaves two workgroups a
+    // CU (40 and more: 8 x 4096 x 2048 97 us, with 32 86).  Where one workgroup
+    // holds the sequence with 8 there are no links, and the lanes' runs count:
+    // 64 x 16 x 2048 bf16 forward 8.8 us with 8, 11.3 with 32; adjoint 13.3, 17.7.
+    return with(len <= 1 ? 1 : len <= WAVES * SHORT ? SHORT : adjoint ? LONG_ADJOINT : LONG);
 }
 
 int64_t links_of(chol_dtype dt, const Plan &p, int64_t batch)
