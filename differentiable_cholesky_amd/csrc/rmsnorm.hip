@@ -65,6 +65,9 @@ template <typename T, int TPR, int NV> struct Row {
 struct Sum {
     static __device__ __forceinline__ float of(float a, float b) { return a + b; }
 };
+struct Max {
+    static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
+};
 // largest magnitude by its bits: as integers, finite < inf < NaN
 struct MaxBits {
     static __device__ __forceinline__ unsigned of(unsigned a, unsigned b) { return a > b ? a : b; }
@@ -111,9 +114,12 @@ template <int V> __device__ __forceinline__ void store_e4m3(unsigned char *p, co
 template <typename T, int TPR, int NV, bool QUANT>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
 {
+    // the low parts below are what a rounded product lost
+#pragma clang fp contract(off)
     constexpr int V = vec_of<T>, BLOCK = TPR < 256 ? 256 : TPR;
     __shared__ float s_sum[TPR > WAVE ? TPR / WAVE : 1];
     __shared__ unsigned s_max[TPR > WAVE ? TPR / WAVE : 1];
+    __shared__ float s_low[TPR > WAVE ? TPR / WAVE : 1];
     const int t = threadIdx.x % TPR, cols = (int)a.cols;
     const int64_t row = (int64_t)blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;
     if (row >= a.rows) // whole waves; rows of more than a wave fill their block
@@ -148,10 +154,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
                 h.set(i, k, h.at(i, k) * s * w.at(i, k));
         h.store((T *)a.y + row * a.ldy, t, cols);
     } else {
-        // s is common to the row: a code is h w / max |h w| * 448, which leaves s's
-        // rounding to the scale alone
-        float y[NV][V];
+        // s is common to the row: a code is h w / max |h w| * 448.  That is formed in
+        // two parts, so that the value a code is rounded from is right to half a step
+        // of fp32: the product's low part (exactly zero for 16-bit types), that of
+        // the largest, and that of 448 over it.
+        constexpr bool LOW = sizeof(T) == 4;
+        float y[NV][V], low[NV];
         unsigned most[NV];
+        const auto low_part = [&](int i, int k) { return LOW ? fmaf(h.at(i, k), w.at(i, k), -y[i][k]) : 0.f; };
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             most[i] = 0;
@@ -161,9 +171,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
                 most[i] = MaxBits::of(most[i], __float_as_uint(y[i][k]) & 0x7fffffffu);
             }
         }
+        // a group is `lanes` neighbouring vectors of one wave
+        const int lanes = a.group / V;
         if (a.group) {
-            // a group is `lanes` neighbouring vectors of one wave
-            const int lanes = a.group / V;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 for (int o = 1; o < lanes; o *= 2)
@@ -173,6 +183,27 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
             for (int i = 1; i < NV; ++i)
                 most[0] = MaxBits::of(most[0], most[i]);
             most[0] = over_row<TPR, MaxBits>(most[0], t, s_max);
+        }
+        if constexpr (LOW) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                low[i] = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if ((__float_as_uint(y[i][k]) & 0x7fffffffu) == most[a.group ? i : 0])
+                        low[i] = fmaxf(low[i], y[i][k] < 0.f ? -low_part(i, k) : low_part(i, k));
+            }
+            if (a.group) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    for (int o = 1; o < lanes; o *= 2)
+                        low[i] = fmaxf(low[i], __shfl_xor(low[i], o));
+            } else {
+#pragma unroll
+                for (int i = 1; i < NV; ++i)
+                    low[0] = fmaxf(low[0], low[i]);
+                low[0] = over_row<TPR, Max>(low[0], t, s_low);
+            }
         }
         unsigned char *q = (unsigned char *)a.y + row * a.ldy;
         float *scale = a.scale + row * a.lds;
@@ -185,10 +216,19 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
             const bool some = top > 0.f;
             const float sc = some ? fmaxf(__fdiv_rn(top, E4M3_MAX), 0x1p-126f) : 1.f;
             const bool plain = some && sc > 0x1p-126f && m > 0x1p-110f; // 448 / m is finite
-            const float pre = plain ? 1.f : s, inv = __fdiv_rn(plain ? E4M3_MAX : 1.f, plain ? m : sc);
+            const float inv = __fdiv_rn(plain ? E4M3_MAX : 1.f, plain ? m : sc);
+            float inv_low = 0.f;
+            if (plain && m < INFINITY) {
+                inv_low = fmaf(-inv, m, E4M3_MAX);
+                if constexpr (LOW)
+                    inv_low = fmaf(-inv, low[a.group ? i : 0], inv_low);
+                inv_low *= inv * (1.f / E4M3_MAX);
+            }
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-                y[i][k] = y[i][k] * pre * inv;
+            for (int k = 0; k < V; ++k) {
+                const float x = plain ? y[i][k] : y[i][k] * s, hi = x * inv;
+                y[i][k] = hi + fmaf(x, inv_low, fmaf(x, inv, -hi) + (plain ? low_part(i, k) * inv : 0.f));
+            }
             if (c < cols) {
                 store_e4m3<V>(q + c, y[i], cols - c);
                 if (a.group ? c % a.group == 0 : c == 0)

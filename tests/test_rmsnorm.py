@@ -68,6 +68,21 @@ def test_quant(rows, cols, dtype, group):
     check_quant(unit64(h) * w.double(), q, scale, group, "quant")
 
 
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(500, 1003), (64, 4096), (3000, 130)])
+def test_codes_are_those_of_64_bits(rows, cols, dtype, group):
+    """A code is rounded from a value that is right to half a step of fp32."""
+    import differentiable_cholesky_amd as dc
+    x, _, w, _, _ = make(rows, cols, dtype, seed=8)
+    q, _, _ = dc.chol_rmsnorm_quant(x, w, group=group, eps=EPS)
+    p = x.double() * w.double()
+    size = group or cols
+    most = torch.nn.functional.pad(p.abs(), (0, -cols % size)).view(rows, -1, size).amax(2)
+    code = (p * (448 / most).repeat_interleave(size, 1)[:, :cols]).float().to(E4M3)
+    assert torch.equal(q.view(torch.uint8), code.view(torch.uint8))
+
+
 def test_quant_of_zeros_nan_and_tiny_rows():
     import differentiable_cholesky_amd as dc
     x, _, w, _, _ = make(5, 300, torch.float32, seed=2)
