@@ -19,8 +19,6 @@ namespace {
 
 constexpr int WAVE = 64;
 constexpr float E4M3_MAX = 448.f;
-// blocks of the adjoint's grid: each leaves one row of partial sums of adj_w
-constexpr int ADJ_BLOCKS = 512;
 
 template <typename T> constexpr int vec_of = 16 / (int)sizeof(T);
 
@@ -78,7 +76,7 @@ struct MaxBits {
 template <int TPR, typename Op, typename S> __device__ __forceinline__ S over_row(S x, int t, S *slot)
 {
 #pragma unroll
-    for (int o = WAVE / 2; o > 0; o /= 2)
+    for (int o = (TPR < WAVE ? TPR : WAVE) / 2; o > 0; o /= 2)
         x = Op::of(x, __shfl_xor(x, o));
     if constexpr (TPR > WAVE) {
         if (t % WAVE == 0)
@@ -112,7 +110,7 @@ template <int V> __device__ __forceinline__ void store_e4m3(unsigned char *p, co
 }
 
 template <typename T, int TPR, int NV, bool QUANT>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a, int64_t first)
 {
     // the low parts below are what a rounded product lost
 #pragma clang fp contract(off)
@@ -121,8 +119,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
     __shared__ unsigned s_max[TPR > WAVE ? TPR / WAVE : 1];
     __shared__ float s_low[TPR > WAVE ? TPR / WAVE : 1];
     const int t = threadIdx.x % TPR, cols = (int)a.cols;
-    const int64_t row = (int64_t)blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;
-    if (row >= a.rows) // whole waves; rows of more than a wave fill their block
+    const int64_t row = first + (int64_t)blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;
+    if (row >= a.rows) // whole rows: no lane of one that stays is missing
         return;
     Row<T, TPR, NV> h, w;
     h.load((const T *)a.x + row * a.ldx, t, cols);
@@ -171,8 +169,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a)
                 most[i] = MaxBits::of(most[i], __float_as_uint(y[i][k]) & 0x7fffffffu);
             }
         }
-        // a group is `lanes` neighbouring vectors of one wave
-        const int lanes = a.group / V;
+        // a group is `lanes` neighbouring vectors of one wave, or the row
+        const int lanes = a.group / V < TPR ? a.group / V : TPR;
         if (a.group) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -251,13 +249,26 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm_adjoint(NormA
     Row<T, TPR, NV> w;
     w.load((const T *)a.w, t, cols);
     float acc[NV][V] = {};
-    int phase = 0;
-    for (int64_t row = (int64_t)blockIdx.x * RPB + slot; row < a.rows; row += (int64_t)gridDim.x * RPB, phase ^= 1) {
-        Row<T, TPR, NV> h, g, p;
+    // the next row is on its way while this one is summed (16384 x 2048 bf16 52 -> 47
+    // us, 8192 x 8192 107 -> 104), where its registers leave room: not for four
+    // vectors, nor in a workgroup of 1024, which has 128 a thread
+    constexpr bool AHEAD = TPR < 1024 && NV <= 2;
+    Row<T, TPR, NV> h, g, p, next_h, next_g, next_p;
+    const auto fetch = [&](int64_t row, Row<T, TPR, NV> &h, Row<T, TPR, NV> &g, Row<T, TPR, NV> &p) {
         h.load((const T *)a.h + row * a.ldh, t, cols);
         g.load((const T *)a.adj + row * a.lda, t, cols);
         if (a.adj_h)
             p.load((const T *)a.adj_h + row * a.ldah, t, cols);
+    };
+    const int64_t start = (int64_t)blockIdx.x * RPB + slot, ahead = (int64_t)gridDim.x * RPB;
+    if (AHEAD && start < a.rows)
+        fetch(start, h, g, p);
+    int phase = 0;
+    for (int64_t row = start; row < a.rows; row += ahead, phase ^= 1) {
+        if constexpr (!AHEAD)
+            fetch(row, h, g, p);
+        else if (row + ahead < a.rows)
+            fetch(row + ahead, next_h, next_g, next_p);
         float hh = 0.f, gh = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -267,7 +278,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm_adjoint(NormA
                 gh = fmaf(g.at(i, k) * w.at(i, k), h.at(i, k), gh);
             }
 #pragma unroll
-        for (int o = WAVE / 2; o > 0; o /= 2) {
+        for (int o = (TPR < WAVE ? TPR : WAVE) / 2; o > 0; o /= 2) {
             hh += __shfl_xor(hh, o);
             gh += __shfl_xor(gh, o);
         }
@@ -299,6 +310,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm_adjoint(NormA
                 h.set(i, k, d);
             }
         h.store((T *)a.adj_x + row * a.ldax, t, cols);
+        if constexpr (AHEAD)
+            h = next_h, g = next_g, p = next_p;
     }
     if constexpr (RPB > 1) {
         if (slot > 0) {
@@ -311,12 +324,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm_adjoint(NormA
         __syncthreads();
         if (slot > 0)
             return;
+#pragma unroll 3
+        for (int j = 0; j < RPB - 1; ++j)
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-#pragma unroll
-                for (int j = 0; j < RPB - 1; ++j)
+                for (int k = 0; k < V; ++k)
                     acc[i][k] += s_w[j][(i * TPR + t) * V + k];
     }
     const bool one = gridDim.x == 1;
@@ -359,23 +372,38 @@ __global__ void __launch_bounds__(256) k_zero(float *out, int n)
         out[i] = 0.f;
 }
 
-// Runs f(threads of a row, vectors of a thread) for rows of `n` vectors
-template <typename F> chol_status with_shape(int64_t n, F f)
+// Runs f(threads of a row, vectors of a thread) for rows of `n` vectors.  A row
+// takes the fewest threads that hold it, so that short rows fill their waves
+// (131072 x 128 bf16: 16 threads 21 us and 26 for the adjoint, 64 threads 52 and
+// 126), but one vector a thread only up to 256 threads: 2048 x 4096 bf16 10.8 us
+// with 256 threads of two, 12.4 with 512 of one.
+template <typename T, typename F> chol_status with_shape(int64_t n, F f)
 {
     using std::integral_constant;
+    if (n <= 8) return f(integral_constant<int, 8>(), integral_constant<int, 1>());
+    if (n <= 16) return f(integral_constant<int, 16>(), integral_constant<int, 1>());
+    if (n <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
     if (n <= 64) return f(integral_constant<int, 64>(), integral_constant<int, 1>());
     if (n <= 128) return f(integral_constant<int, 64>(), integral_constant<int, 2>());
     if (n <= 256) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
     if (n <= 512) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
-    if (n <= 1024) return f(integral_constant<int, 256>(), integral_constant<int, 4>());
+    if (n <= 1024) return f(integral_constant<int, 512>(), integral_constant<int, 2>());
     if (n <= 2048) return f(integral_constant<int, 1024>(), integral_constant<int, 2>());
-    if (n <= 4096) return f(integral_constant<int, 1024>(), integral_constant<int, 4>());
+    if constexpr (sizeof(T) == 4) // 16-bit rows of the longest kind end above
+        if (n <= 4096) return f(integral_constant<int, 1024>(), integral_constant<int, 4>());
     return CHOL_ERR_NOT_SUPPORTED;
 }
 
 template <typename T> int64_t vectors(int64_t cols) { return (cols + vec_of<T> - 1) / vec_of<T>; }
 
-int64_t adjoint_blocks(int64_t rows, int rpb) { return std::min<int64_t>(ADJ_BLOCKS, (rows + rpb - 1) / rpb); }
+// Each workgroup of the adjoint leaves a row of partial sums of adj_w: few enough
+// that these stay small beside the rows (8192 x 8192 bf16: 104 us with 256
+// workgroups of 512 threads, 109 with 512), enough that the CUs stay full
+// (workgroups of 256: 16384 x 4096 103 us with 512, 116 with 1024).
+int64_t adjoint_blocks(int64_t rows, int rpb, int block)
+{
+    return std::min<int64_t>(block > 256 ? 256 : 512, (rows + rpb - 1) / rpb);
+}
 
 } // namespace
 
@@ -383,14 +411,17 @@ chol_status rmsnorm(chol_dtype dt, bool quantise, const NormArgs &a, hipStream_t
 {
     return with_lowp(dt, [&](auto *e) {
         typedef std::remove_pointer_t<decltype(e)> T;
-        return with_shape(vectors<T>(a.cols), [&](auto tpr, auto nv) {
+        return with_shape<T>(vectors<T>(a.cols), [&](auto tpr, auto nv) {
             constexpr int TPR = tpr, NV = nv, BLOCK = TPR < 256 ? 256 : TPR;
-            const int64_t grid = (a.rows + BLOCK / TPR - 1) / (BLOCK / TPR);
-            if (quantise)
-                hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, true>), dim3((unsigned)grid), dim3(BLOCK), 0, st, a);
-            else
-                hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, false>), dim3((unsigned)grid), dim3(BLOCK), 0, st, a);
-            CHOL_LAUNCH_CHECK();
+            constexpr int64_t RPB = BLOCK / TPR, MOST = (int64_t)1 << 21; // workgroups of a launch: a grid holds < 2^32 threads
+            for (int64_t first = 0; first < a.rows; first += MOST * RPB) {
+                const unsigned grid = (unsigned)std::min(MOST, (a.rows - first + RPB - 1) / RPB);
+                if (quantise)
+                    hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, true>), dim3(grid), dim3(BLOCK), 0, st, a, first);
+                else
+                    hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, false>), dim3(grid), dim3(BLOCK), 0, st, a, first);
+                CHOL_LAUNCH_CHECK();
+            }
             return CHOL_OK;
         });
     });
@@ -401,9 +432,9 @@ size_t rmsnorm_adjoint_workspace(chol_dtype dt, int64_t rows, int64_t cols)
     size_t bytes = 0;
     (void)with_lowp(dt, [&](auto *e) {
         typedef std::remove_pointer_t<decltype(e)> T;
-        return with_shape(vectors<T>(cols), [&](auto tpr, auto) {
+        return with_shape<T>(vectors<T>(cols), [&](auto tpr, auto) {
             constexpr int TPR = tpr, RPB = TPR < 256 ? 256 / TPR : 1;
-            const int64_t blocks = adjoint_blocks(rows, RPB);
+            const int64_t blocks = adjoint_blocks(rows, RPB, TPR < 256 ? 256 : TPR);
             bytes = blocks > 1 ? (size_t)(blocks * cols) * sizeof(float) : 0;
             return CHOL_OK;
         });
@@ -421,9 +452,9 @@ chol_status rmsnorm_adjoint(chol_dtype dt, const NormAdjArgs &a, void *ws, hipSt
     }
     return with_lowp(dt, [&](auto *e) {
         typedef std::remove_pointer_t<decltype(e)> T;
-        return with_shape(vectors<T>(a.cols), [&](auto tpr, auto nv) {
+        return with_shape<T>(vectors<T>(a.cols), [&](auto tpr, auto nv) {
             constexpr int TPR = tpr, NV = nv, BLOCK = TPR < 256 ? 256 : TPR;
-            const int64_t blocks = adjoint_blocks(a.rows, BLOCK / TPR);
+            const int64_t blocks = adjoint_blocks(a.rows, BLOCK / TPR, BLOCK);
             hipLaunchKernelGGL((k_rmsnorm_adjoint<T, TPR, NV>), dim3((unsigned)blocks), dim3(BLOCK), 0, st, a,
                                (float *)ws);
             CHOL_LAUNCH_CHECK();

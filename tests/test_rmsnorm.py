@@ -26,7 +26,7 @@ def unit64(h):
 
 
 SIZES = [(1, 1), (3, 7), (5, 64), (2, 511), (4, 512), (7, 1003), (3, 1024), (2, 2047), (3, 4096), (2, 4100), (1, 8192),
-         (2, 16383), (3, 16384), (600, 136)]
+         (2, 16383), (3, 16384), (600, 136), (100, 32), (77, 33), (50, 128), (33, 129), (19, 256)]
 
 
 @pytest.mark.parametrize("residual", [False, True])
@@ -105,7 +105,7 @@ def test_quant_of_zeros_nan_and_tiny_rows():
     assert torch.isfinite(q.float()[0, 64:]).all()
 
 
-ADJ_SIZES = SIZES + [(513, 520), (2100, 130), (1025, 2050)]
+ADJ_SIZES = SIZES + [(513, 520), (2100, 130), (1025, 2050), (20000, 60), (9000, 90), (5000, 250)]
 
 
 @pytest.mark.parametrize("past", [False, True])
@@ -210,3 +210,14 @@ def test_captured_into_a_graph():
         torch.cuda.synchronize()
         for a, b in zip((y, s, dx, dw), (*want, *grads)):
             assert torch.equal(a, b)
+
+
+def test_more_rows_than_one_launch_takes():
+    import differentiable_cholesky_amd as dc
+    rows, cols = (1 << 26) + 5, 3
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-6:] = torch.randn(6, cols, device="cuda").bfloat16()
+    w = torch.tensor([1.0, 2.0, 0.5], device="cuda").bfloat16()
+    y, _ = dc.chol_rmsnorm(x, w, eps=EPS)
+    assert torch.equal(y[-6:], dc.chol_rmsnorm(x[-6:].clone(), w, eps=EPS)[0])
+    assert torch.equal(y[:-6].amin(0), w) and torch.equal(y[:-6].amax(0), w)
