@@ -174,6 +174,31 @@ def test_states_of_zero_and_non_finite_gradients(bits):
     assert not torch.equal(p[513:700], keep[0][513:700])
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_second_moments_of_every_size(bits):
+    """Roots of values far from one, in tiles of their own and beside ordinary ones."""
+    import differentiable_cholesky_amd as dc
+    n = 4096
+    before = make(torch.float32, False, bits, seed=7, sizes=[n])
+    before["g"][0].zero_()
+    g = torch.Generator().manual_seed(8)
+    place = torch.rand(n // TILE, 1, generator=g) * 2 - 1 + torch.zeros(1, TILE)
+    place[::3] = torch.rand(place[::3].shape, generator=g) * 2 - 1
+    if bits == 32:
+        before["v"] = [torch.pow(10.0, 36 * place.double()).float().view(-1)]
+        before["m"] = [(before["v"][0].double().sqrt() * torch.randn(n, generator=g).double()).float()]
+    else:
+        for k in ("m_scale", "v_scale"):
+            before[k] = [torch.exp2(torch.round(48 * place[:, 0]))]
+    hyper = dict(HYPER, eps=0.0)
+    if bits == 8:
+        before["v"] = [torch.clamp(before["v"][0].view(torch.uint8), min=1).view(E4M3)]
+    t, _ = on_gpu(before)
+    handle = dc.chol_adamw_list(t["p"], t["g"], t["m"], t["v"], m_scale=t.get("m_scale"), v_scale=t.get("v_scale"))
+    dc.chol_adamw(handle, seed=11, **hyper)
+    check(before, t, False, bits, 1.0, 11, [0], hyper)
+
+
 def test_eight_bit_states_are_unbiased():
     """The mean over seeds of a stored state is the state: no more than 6 standard deviations of a step's rounding off."""
     import differentiable_cholesky_amd as dc
