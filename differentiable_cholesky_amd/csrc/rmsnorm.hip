@@ -22,18 +22,28 @@ constexpr float E4M3_MAX = 448.f;
 
 template <typename T> constexpr int vec_of = 16 / (int)sizeof(T);
 
+// A call that moves well over the 256 MB which the last cache holds reads past it
+// (STREAM), and leaves it to what is written.  Norm of n x 4096 bf16 between a
+// kernel that writes its input and one that reads its output, us for the three:
+// 16384 rows 177 -> 167, 12288 (403 MB) 130 -> 127, but 8192 (268 MB) 86 -> 90.
+constexpr double CACHE = 320e6;
+
 // NV vectors of one row, thread `t` of TPR holding vectors t, t + TPR, ...; zero
 // past the end of the row.
 template <typename T, int TPR, int NV> struct Row {
     static constexpr int V = vec_of<T>;
     vec<T, V> v[NV];
-    __device__ __forceinline__ void load(const T *p, int t, int cols)
+    template <bool STREAM> __device__ __forceinline__ void load(const T *p, int t, int cols)
     {
+        typedef unsigned any __attribute__((ext_vector_type(4), aligned(2)));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * V;
             if (c + V <= cols) {
-                v[i] = load_vec<T, V>(p + c);
+                if constexpr (STREAM)
+                    v[i] = __builtin_bit_cast(vec<T, V>, __builtin_nontemporal_load((const any *)(p + c)));
+                else
+                    v[i] = load_vec<T, V>(p + c);
             } else {
 #pragma unroll
                 for (int k = 0; k < V; ++k)
@@ -109,7 +119,7 @@ template <int V> __device__ __forceinline__ void store_e4m3(unsigned char *p, co
     }
 }
 
-template <typename T, int TPR, int NV, bool QUANT>
+template <typename T, int TPR, int NV, bool QUANT, bool STREAM>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a, int64_t first)
 {
     // the low parts below are what a rounded product lost
@@ -123,11 +133,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a, i
     if (row >= a.rows) // whole rows: no lane of one that stays is missing
         return;
     Row<T, TPR, NV> h, w;
-    h.load((const T *)a.x + row * a.ldx, t, cols);
+    h.template load<STREAM>((const T *)a.x + row * a.ldx, t, cols);
     if (a.residual) {
         Row<T, TPR, NV> r;
-        r.load((const T *)a.residual + row * a.ldr, t, cols);
-        w.load((const T *)a.w, t, cols);
+        r.template load<STREAM>((const T *)a.residual + row * a.ldr, t, cols);
+        w.template load<false>((const T *)a.w, t, cols);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -135,7 +145,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a, i
                 h.set(i, k, h.at(i, k) + r.at(i, k));
         h.store((T *)a.h + row * a.ldh, t, cols);
     } else {
-        w.load((const T *)a.w, t, cols);
+        w.template load<false>((const T *)a.w, t, cols);
     }
     float sum = 0.f;
 #pragma unroll
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a, i
 // Rows blockIdx.x * RPB + slot, then a grid further on; every thread sums its
 // columns' adj h s over its rows.  part[blockIdx.x * cols + c], or adj_w itself
 // where the grid is one block.
-template <typename T, int TPR, int NV>
+template <typename T, int TPR, int NV, bool STREAM>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm_adjoint(NormAdjArgs a, float *part)
 {
     constexpr int V = vec_of<T>, BLOCK = TPR < 256 ? 256 : TPR, RPB = BLOCK / TPR;
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm_adjoint(NormA
     __shared__ float s_w[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? TPR * NV * V : 1];
     const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR, cols = (int)a.cols;
     Row<T, TPR, NV> w;
-    w.load((const T *)a.w, t, cols);
+    w.template load<false>((const T *)a.w, t, cols);
     float acc[NV][V] = {};
     // the next row is on its way while this one is summed (16384 x 2048 bf16 52 -> 47
     // us, 8192 x 8192 107 -> 104), where its registers leave room: not for four
@@ -255,10 +265,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm_adjoint(NormA
     constexpr bool AHEAD = TPR < 1024 && NV <= 2;
     Row<T, TPR, NV> h, g, p, next_h, next_g, next_p;
     const auto fetch = [&](int64_t row, Row<T, TPR, NV> &h, Row<T, TPR, NV> &g, Row<T, TPR, NV> &p) {
-        h.load((const T *)a.h + row * a.ldh, t, cols);
-        g.load((const T *)a.adj + row * a.lda, t, cols);
+        h.template load<STREAM>((const T *)a.h + row * a.ldh, t, cols);
+        g.template load<STREAM>((const T *)a.adj + row * a.lda, t, cols);
         if (a.adj_h)
-            p.load((const T *)a.adj_h + row * a.ldah, t, cols);
+            p.template load<STREAM>((const T *)a.adj_h + row * a.ldah, t, cols);
     };
     const int64_t start = (int64_t)blockIdx.x * RPB + slot, ahead = (int64_t)gridDim.x * RPB;
     if (AHEAD && start < a.rows)
@@ -414,12 +424,17 @@ chol_status rmsnorm(chol_dtype dt, bool quantise, const NormArgs &a, hipStream_t
         return with_shape<T>(vectors<T>(a.cols), [&](auto tpr, auto nv) {
             constexpr int TPR = tpr, NV = nv, BLOCK = TPR < 256 ? 256 : TPR;
             constexpr int64_t RPB = BLOCK / TPR, MOST = (int64_t)1 << 21; // workgroups of a launch: a grid holds < 2^32 threads
+            const double size = (a.residual ? 3.0 : 1.0) * sizeof(T) + (quantise ? 1 : sizeof(T));
+            const bool stream = size * a.rows * a.cols > CACHE;
             for (int64_t first = 0; first < a.rows; first += MOST * RPB) {
                 const unsigned grid = (unsigned)std::min(MOST, (a.rows - first + RPB - 1) / RPB);
+                const auto launch = [&](auto kernel) {
+                    hipLaunchKernelGGL(kernel, dim3(grid), dim3(BLOCK), 0, st, a, first);
+                };
                 if (quantise)
-                    hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, true>), dim3(grid), dim3(BLOCK), 0, st, a, first);
+                    stream ? launch(k_rmsnorm<T, TPR, NV, true, true>) : launch(k_rmsnorm<T, TPR, NV, true, false>);
                 else
-                    hipLaunchKernelGGL((k_rmsnorm<T, TPR, NV, false>), dim3(grid), dim3(BLOCK), 0, st, a, first);
+                    stream ? launch(k_rmsnorm<T, TPR, NV, false, true>) : launch(k_rmsnorm<T, TPR, NV, false, false>);
                 CHOL_LAUNCH_CHECK();
             }
             return CHOL_OK;
@@ -455,8 +470,11 @@ chol_status rmsnorm_adjoint(chol_dtype dt, const NormAdjArgs &a, void *ws, hipSt
         return with_shape<T>(vectors<T>(a.cols), [&](auto tpr, auto nv) {
             constexpr int TPR = tpr, NV = nv, BLOCK = TPR < 256 ? 256 : TPR;
             const int64_t blocks = adjoint_blocks(a.rows, BLOCK / TPR, BLOCK);
-            hipLaunchKernelGGL((k_rmsnorm_adjoint<T, TPR, NV>), dim3((unsigned)blocks), dim3(BLOCK), 0, st, a,
-                               (float *)ws);
+            const auto launch = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(BLOCK), 0, st, a, (float *)ws);
+            };
+            const bool stream = (a.adj_h ? 4.0 : 3.0) * sizeof(T) * a.rows * a.cols > CACHE;
+            stream ? launch(k_rmsnorm_adjoint<T, TPR, NV, true>) : launch(k_rmsnorm_adjoint<T, TPR, NV, false>);
             CHOL_LAUNCH_CHECK();
             if (blocks > 1) {
                 hipLaunchKernelGGL(k_sum_rows, dim3((unsigned)((a.cols + WAVE - 1) / WAVE)), dim3(1024), 0, st,

@@ -221,3 +221,19 @@ def test_more_rows_than_one_launch_takes():
     y, _ = dc.chol_rmsnorm(x, w, eps=EPS)
     assert torch.equal(y[-6:], dc.chol_rmsnorm(x[-6:].clone(), w, eps=EPS)[0])
     assert torch.equal(y[:-6].amin(0), w) and torch.equal(y[:-6].amax(0), w)
+
+
+def test_rows_beyond_the_caches():
+    """A call that moves more than the last cache holds gives what its slices give."""
+    import differentiable_cholesky_amd as dc
+    rows, cols = 9000, 4100
+    x, r, w, adj, adj_h = (t.cuda() for t in make(rows, cols, torch.bfloat16, seed=9))
+    y, h = dc.chol_rmsnorm(x, w, residual=r)
+    q, scale, _ = dc.chol_rmsnorm_quant(x, w, residual=r, group=64)
+    dx, _ = dc.chol_rmsnorm_adjoint(h, w, adj, adjH=adj_h)
+    for part in (slice(0, 2500), slice(2500, 5000), slice(5000, 7500), slice(7500, rows)):
+        y1, h1 = dc.chol_rmsnorm(x[part], w, residual=r[part])
+        assert torch.equal(y1, y[part]) and torch.equal(h1, h[part])
+        q1, s1, _ = dc.chol_rmsnorm_quant(x[part], w, residual=r[part], group=64)
+        assert torch.equal(q1.float(), q[part].float()) and torch.equal(s1, scale[part])
+        assert torch.equal(dc.chol_rmsnorm_adjoint(h1, w, adj[part], adjH=adj_h[part])[0], dx[part])
