@@ -56,6 +56,9 @@ def _code(t) -> int:
 
 def _same(t, name: str, like, shape=None, dtype=None):
     """t is on like's device and has the given shape (default like's) and type (default like's)."""
+    if t.shape == (like.shape if shape is None else shape) and t.dtype is (like.dtype if dtype is None else dtype) \
+            and t.device == like.device:
+        return
     if t.device != like.device:
         raise ValueError(f"{name} must live on {like.device}, got {t.device}")
     if t.dtype != (like.dtype if dtype is None else dtype):
@@ -161,7 +164,7 @@ def chol_recurrence(a, b, h0=None, hlast=None, h=None, gate: str = "linear", wor
         else:
             _same(h, "h", a)
         if hlast is None:
-            hlast = torch.empty((batch, dim), dtype=torch.float32, device=a.device)
+            hlast = a.new_empty((batch, dim), dtype=torch.float32)
         ph0, pl = _state(h0, "h0", a, (batch, dim)), _state(hlast, "hlast", a, (batch, dim))
         need = chol_recurrence_workspace_size(code, batch, length, dim) if length > 1 else 0
         keep, ws, wbytes = _scratch(need, a.device, workspace)
@@ -193,7 +196,7 @@ def chol_recurrence_adjoint(a, h, adjH, h0=None, adjHlast=None, adjA=None, adjB=
         else:
             _same(adjB, "adjB", a)
         if adjH0 is None:
-            adjH0 = torch.empty((batch, dim), dtype=torch.float32, device=a.device)
+            adjH0 = a.new_empty((batch, dim), dtype=torch.float32)
         ph0 = _state(h0, "h0", a, (batch, dim))
         pl, p0 = _state(adjHlast, "adjHlast", a, (batch, dim)), _state(adjH0, "adjH0", a, (batch, dim))
         need = chol_recurrence_workspace_size(code, batch, length, dim) if length > 1 else 0
@@ -212,15 +215,15 @@ RMSNORM_GROUPS = (0, 32, 64, 128, 256)
 def _rows(t, name: str):
     """(pointer, ld) of a [rows, cols] array with unit column stride, or of any
     contiguous array taken as rows of its last dimension."""
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[-1]
     if t.dim() == 2:
         ld, sc = t.stride()
         rows, cols = t.shape
         if cols > 1 and sc != 1:
             raise ValueError(f"{name} must have unit column stride")
         return t.data_ptr(), ld if rows > 1 else cols
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be [rows, cols] or contiguous")
-    return t.data_ptr(), t.shape[-1]
+    raise ValueError(f"{name} must be [rows, cols] or contiguous")
 
 
 def _row_shape(x, w):
@@ -280,7 +283,7 @@ def chol_rmsnorm_quant(x, w, residual=None, group: int = 0, eps: float = 1e-6, q
         else:
             _same(q, "q", x, dtype=torch.float8_e4m3fn)
         if scale is None:
-            scale = torch.empty((rows, groups), dtype=torch.float32, device=x.device)
+            scale = x.new_empty((rows, groups), dtype=torch.float32)
         else:
             _same(scale, "scale", x, (rows, groups), torch.float32)
         pq, ldq = _rows(q, "q")
@@ -322,7 +325,7 @@ def chol_rmsnorm_adjoint(h, w, adj, adjH=None, eps: float = 1e-6, adjX=None, adj
         else:
             _same(adjX, "adjX", h)
         if adjW is None:
-            adjW = (torch.zeros if accumulate else torch.empty)((cols,), dtype=torch.float32, device=h.device)
+            adjW = (h.new_zeros if accumulate else h.new_empty)((cols,), dtype=torch.float32)
         else:
             _state(adjW, "adjW", h, (cols,))
         ph, ldh = _rows(h, "h")
