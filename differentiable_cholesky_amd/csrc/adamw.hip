@@ -16,8 +16,10 @@
 // bf16 with fp32 master, us with 32-bit and with 8-bit states:
 //   a workgroup of 256 that walks 4096 elements           1670   987
 //   the same without the caches                           1590   949
-//   a workgroup of 256 for 1024 elements, then of 64      1423   929,  1351   907
-// (6.3 and 5.4 TB/s; a copy reaches 5.2).  With 8-bit states the arithmetic of the
+//   a workgroup of 256 for 1024 elements                  1423   929
+//   of 64 for 256                                         1351   907
+//   and the tile's largest over the lanes without LDS     1352   871
+// (6.3 and 5.6 TB/s; a copy reaches 5.2).  With 8-bit states the arithmetic of the
 // codes and the random bits takes nearly as long as the memory.
 #include <algorithm>
 #include <type_traits>
@@ -158,6 +160,19 @@ __device__ __forceinline__ void roots(const float (&x)[V], float (&root)[V])
     }
 }
 
+// largest of the wave's values, in every lane: over the 16 lanes of a row, then
+// rows 0 and 2 into 1 and 3, and 1 into 3
+__device__ __forceinline__ unsigned wave_max(unsigned x)
+{
+    x = max(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0xb1, 0xf, 0xf, false));  // lanes xor 1
+    x = max(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x4e, 0xf, 0xf, false));  // lanes xor 2
+    x = max(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xf, 0xf, false)); // mirror of 8
+    x = max(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xf, 0xf, false)); // mirror of 16
+    x = max(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xa, 0xf, false));
+    x = max(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xc, 0xf, false));
+    return (unsigned)__builtin_amdgcn_readlane((int)x, 63);
+}
+
 // Codes and scale of a tile held by the wave
 __device__ __forceinline__ void write_codes(void *base, float *scale, uint32_t at, int n, const float (&x)[V],
                                             const unsigned (&noise)[V], bool keep)
@@ -166,9 +181,7 @@ __device__ __forceinline__ void write_codes(void *base, float *scale, uint32_t a
 #pragma unroll
     for (int k = 0; k < V; ++k)
         most = max(most, __float_as_uint(x[k]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = 32; o > 0; o /= 2)
-        most = max(most, (unsigned)__shfl_xor((int)most, o));
+    most = wave_max(most);
     const int e = max((int)(most >> 23) - 7, 1);
     const float inv = __uint_as_float((unsigned)(254 - e) << 23);
     unsigned u = 0;

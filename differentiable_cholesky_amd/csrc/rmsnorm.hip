@@ -21,6 +21,8 @@ constexpr int WAVE = 64;
 constexpr float E4M3_MAX = 448.f;
 
 template <typename T> constexpr int vec_of = 16 / (int)sizeof(T);
+// threads of a workgroup: a row of more than a wave has its own, whose LDS it uses
+template <int TPR> constexpr int block_of = TPR > WAVE ? TPR : 256;
 
 // A call that moves well over the 256 MB which the last cache holds reads past it
 // (STREAM), and leaves it to what is written.  Norm of n x 4096 bf16 between a
@@ -120,11 +122,11 @@ template <int V> __device__ __forceinline__ void store_e4m3(unsigned char *p, co
 }
 
 template <typename T, int TPR, int NV, bool QUANT, bool STREAM>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a, int64_t first)
+__global__ void __launch_bounds__(block_of<TPR>) k_rmsnorm(NormArgs a, int64_t first)
 {
     // the low parts below are what a rounded product lost
 #pragma clang fp contract(off)
-    constexpr int V = vec_of<T>, BLOCK = TPR < 256 ? 256 : TPR;
+    constexpr int V = vec_of<T>, BLOCK = block_of<TPR>;
     __shared__ float s_sum[TPR > WAVE ? TPR / WAVE : 1];
     __shared__ unsigned s_max[TPR > WAVE ? TPR / WAVE : 1];
     __shared__ float s_low[TPR > WAVE ? TPR / WAVE : 1];
@@ -250,9 +252,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm(NormArgs a, i
 // columns' adj h s over its rows.  part[blockIdx.x * cols + c], or adj_w itself
 // where the grid is one block.
 template <typename T, int TPR, int NV, bool STREAM>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm_adjoint(NormAdjArgs a, float *part)
+__global__ void __launch_bounds__(block_of<TPR>) k_rmsnorm_adjoint(NormAdjArgs a, float *part)
 {
-    constexpr int V = vec_of<T>, BLOCK = TPR < 256 ? 256 : TPR, RPB = BLOCK / TPR;
+    constexpr int V = vec_of<T>, BLOCK = block_of<TPR>, RPB = BLOCK / TPR;
     __shared__ float s_sum[2][TPR > WAVE ? 2 * TPR / WAVE : 1];
     __shared__ float s_w[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? TPR * NV * V : 1];
     const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR, cols = (int)a.cols;
@@ -354,21 +356,25 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rmsnorm_adjoint(NormA
         }
 }
 
-// adj_w[c] (+)= the sum of `count` rows of partial sums, in a fixed order: 16
-// waves take every 16th row, and their sums are added in LDS.
-__global__ void __launch_bounds__(1024) k_sum_rows(const float *part, int count, int cols, float *out, int accumulate)
+// adj_w[c] (+)= the sum of `count` rows of partial sums, in a fixed order: of the
+// 64 threads of a column each takes every 64th row, and their sums are added in
+// LDS.
+constexpr int SUM_COLS = 16, SUM_PARTS = 64;
+
+__global__ void __launch_bounds__(SUM_COLS *SUM_PARTS) k_sum_rows(const float *part, int count, int cols, float *out,
+                                                                  int accumulate)
 {
-    __shared__ float s[16][WAVE];
-    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE, c = (int)blockIdx.x * WAVE + lane;
+    __shared__ float s[SUM_PARTS][SUM_COLS];
+    const int lane = threadIdx.x % SUM_COLS, p = threadIdx.x / SUM_COLS, c = (int)blockIdx.x * SUM_COLS + lane;
     float x = 0.f;
     if (c < cols)
 #pragma unroll 8
-        for (int r = wave; r < count; r += 16)
+        for (int r = p; r < count; r += SUM_PARTS)
             x += part[(int64_t)r * cols + c];
-    s[wave][lane] = x;
+    s[p][lane] = x;
     __syncthreads();
-    if (wave == 0 && c < cols) {
-        for (int i = 1; i < 16; ++i)
+    if (p == 0 && c < cols) {
+        for (int i = 1; i < SUM_PARTS; ++i)
             x += s[i][lane];
         out[c] = accumulate ? out[c] + x : x;
     }
@@ -385,8 +391,10 @@ __global__ void __launch_bounds__(256) k_zero(float *out, int n)
 // Runs f(threads of a row, vectors of a thread) for rows of `n` vectors.  A row
 // takes the fewest threads that hold it, so that short rows fill their waves
 // (131072 x 128 bf16: 16 threads 21 us and 26 for the adjoint, 64 threads 52 and
-// 126), but one vector a thread only up to 256 threads: 2048 x 4096 bf16 10.8 us
-// with 256 threads of two, 12.4 with 512 of one.
+// 126), and several vectors a thread before more threads: 2048 x 4096 bf16 10.8 us
+// with 256 threads of two, 12.4 with 512 of one.  Up to 256 vectors a wave alone
+// holds the row: the adjoint of 16384 x 1500 53 us, of 16384 x 2048 55, with 256
+// threads 123 and 53 (most of the difference is the ragged end, which waits).
 template <typename T, typename F> chol_status with_shape(int64_t n, F f)
 {
     using std::integral_constant;
@@ -395,7 +403,7 @@ template <typename T, typename F> chol_status with_shape(int64_t n, F f)
     if (n <= 32) return f(integral_constant<int, 32>(), integral_constant<int, 1>());
     if (n <= 64) return f(integral_constant<int, 64>(), integral_constant<int, 1>());
     if (n <= 128) return f(integral_constant<int, 64>(), integral_constant<int, 2>());
-    if (n <= 256) return f(integral_constant<int, 256>(), integral_constant<int, 1>());
+    if (n <= 256) return f(integral_constant<int, 64>(), integral_constant<int, 4>());
     if (n <= 512) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
     if (n <= 1024) return f(integral_constant<int, 512>(), integral_constant<int, 2>());
     if (n <= 2048) return f(integral_constant<int, 1024>(), integral_constant<int, 2>());
@@ -410,9 +418,10 @@ template <typename T> int64_t vectors(int64_t cols) { return (cols + vec_of<T> -
 // that these stay small beside the rows (8192 x 8192 bf16: 104 us with 256
 // workgroups of 512 threads, 109 with 512), enough that the CUs stay full
 // (workgroups of 256: 16384 x 4096 103 us with 512, 116 with 1024).
-int64_t adjoint_blocks(int64_t rows, int rpb, int block)
+template <int TPR> int64_t adjoint_blocks(int64_t rows)
 {
-    return std::min<int64_t>(block > 256 ? 256 : 512, (rows + rpb - 1) / rpb);
+    constexpr int64_t rpb = block_of<TPR> / TPR;
+    return std::min<int64_t>(block_of<TPR> > 256 ? 256 : 512, (rows + rpb - 1) / rpb);
 }
 
 } // namespace
@@ -422,7 +431,7 @@ chol_status rmsnorm(chol_dtype dt, bool quantise, const NormArgs &a, hipStream_t
     return with_lowp(dt, [&](auto *e) {
         typedef std::remove_pointer_t<decltype(e)> T;
         return with_shape<T>(vectors<T>(a.cols), [&](auto tpr, auto nv) {
-            constexpr int TPR = tpr, NV = nv, BLOCK = TPR < 256 ? 256 : TPR;
+            constexpr int TPR = tpr, NV = nv, BLOCK = block_of<TPR>;
             constexpr int64_t RPB = BLOCK / TPR, MOST = (int64_t)1 << 21; // workgroups of a launch: a grid holds < 2^32 threads
             const double size = (a.residual ? 3.0 : 1.0) * sizeof(T) + (quantise ? 1 : sizeof(T));
             const bool stream = size * a.rows * a.cols > CACHE;
@@ -448,8 +457,8 @@ size_t rmsnorm_adjoint_workspace(chol_dtype dt, int64_t rows, int64_t cols)
     (void)with_lowp(dt, [&](auto *e) {
         typedef std::remove_pointer_t<decltype(e)> T;
         return with_shape<T>(vectors<T>(cols), [&](auto tpr, auto) {
-            constexpr int TPR = tpr, RPB = TPR < 256 ? 256 / TPR : 1;
-            const int64_t blocks = adjoint_blocks(rows, RPB, TPR < 256 ? 256 : TPR);
+            constexpr int TPR = tpr;
+            const int64_t blocks = adjoint_blocks<TPR>(rows);
             bytes = blocks > 1 ? (size_t)(blocks * cols) * sizeof(float) : 0;
             return CHOL_OK;
         });
@@ -468,8 +477,8 @@ chol_status rmsnorm_adjoint(chol_dtype dt, const NormAdjArgs &a, void *ws, hipSt
     return with_lowp(dt, [&](auto *e) {
         typedef std::remove_pointer_t<decltype(e)> T;
         return with_shape<T>(vectors<T>(a.cols), [&](auto tpr, auto nv) {
-            constexpr int TPR = tpr, NV = nv, BLOCK = TPR < 256 ? 256 : TPR;
-            const int64_t blocks = adjoint_blocks(a.rows, BLOCK / TPR, BLOCK);
+            constexpr int TPR = tpr, NV = nv, BLOCK = block_of<TPR>;
+            const int64_t blocks = adjoint_blocks<TPR>(a.rows);
             const auto launch = [&](auto kernel) {
                 hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(BLOCK), 0, st, a, (float *)ws);
             };
@@ -477,7 +486,7 @@ chol_status rmsnorm_adjoint(chol_dtype dt, const NormAdjArgs &a, void *ws, hipSt
             stream ? launch(k_rmsnorm_adjoint<T, TPR, NV, true>) : launch(k_rmsnorm_adjoint<T, TPR, NV, false>);
             CHOL_LAUNCH_CHECK();
             if (blocks > 1) {
-                hipLaunchKernelGGL(k_sum_rows, dim3((unsigned)((a.cols + WAVE - 1) / WAVE)), dim3(1024), 0, st,
+                hipLaunchKernelGGL(k_sum_rows, dim3((unsigned)((a.cols + SUM_COLS - 1) / SUM_COLS)), dim3(SUM_COLS * SUM_PARTS), 0, st,
                                    (const float *)ws, (int)blocks, (int)a.cols, a.adj_w, a.accumulate);
                 CHOL_LAUNCH_CHECK();
             }

@@ -155,6 +155,22 @@ def test_norm_adjoint_refusals(change, expect):
     assert norm_adjoint(**change) == expect
 
 
+def test_norm_adjoint_workspace_size():
+    """A row of partial sums for every workgroup but a single one; a workgroup takes the rows that its threads hold."""
+    def size(dt, rows, cols):
+        out = ctypes.c_size_t(0)
+        assert lib.chol_rmsnorm_adjoint_workspace_size(dt, rows, cols, ctypes.byref(out)) == OK
+        return out.value
+
+    for dt, width in ((BF16, 8), (F16, 8), (F32, 4)):
+        for cols in (1, 64, 100, 128, 250, 300, 511, 512, 1000, 1024, 1025, 2000, 2047, 2048, 3000, 4096, 5000, 8192, 16384):
+            vectors = -(-cols // width)
+            together = 1 if vectors > 128 else 256 // min(t for t in (8, 16, 32, 64) if t >= min(vectors, 64))
+            assert size(dt, 1, cols) == size(dt, together, cols) == 0
+            assert size(dt, together + 1, cols) == 2 * cols * 4
+            assert size(dt, 1 << 20, cols) in (256 * cols * 4, 512 * cols * 4)
+
+
 def test_norm_binding_refuses():
     x, w = torch.zeros(3, 8), torch.ones(8)
     with pytest.raises(ValueError):
