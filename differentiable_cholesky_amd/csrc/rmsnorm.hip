@@ -356,25 +356,21 @@ __global__ void __launch_bounds__(block_of<TPR>) k_rmsnorm_adjoint(NormAdjArgs a
         }
 }
 
-// adj_w[c] (+)= the sum of `count` rows of partial sums, in a fixed order: of the
-// 64 threads of a column each takes every 64th row, and their sums are added in
-// LDS.
-constexpr int SUM_COLS = 16, SUM_PARTS = 64;
-
-__global__ void __launch_bounds__(SUM_COLS *SUM_PARTS) k_sum_rows(const float *part, int count, int cols, float *out,
-                                                                  int accumulate)
+// adj_w[c] (+)= the sum of `count` rows of partial sums, in a fixed order: 16
+// waves take every 16th row, and their sums are added in LDS.
+__global__ void __launch_bounds__(1024) k_sum_rows(const float *part, int count, int cols, float *out, int accumulate)
 {
-    __shared__ float s[SUM_PARTS][SUM_COLS];
-    const int lane = threadIdx.x % SUM_COLS, p = threadIdx.x / SUM_COLS, c = (int)blockIdx.x * SUM_COLS + lane;
+    __shared__ float s[16][WAVE];
+    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE, c = (int)blockIdx.x * WAVE + lane;
     float x = 0.f;
     if (c < cols)
 #pragma unroll 8
-        for (int r = p; r < count; r += SUM_PARTS)
+        for (int r = wave; r < count; r += 16)
             x += part[(int64_t)r * cols + c];
-    s[p][lane] = x;
+    s[wave][lane] = x;
     __syncthreads();
-    if (p == 0 && c < cols) {
-        for (int i = 1; i < SUM_PARTS; ++i)
+    if (wave == 0 && c < cols) {
+        for (int i = 1; i < 16; ++i)
             x += s[i][lane];
         out[c] = accumulate ? out[c] + x : x;
     }
@@ -486,7 +482,7 @@ chol_status rmsnorm_adjoint(chol_dtype dt, const NormAdjArgs &a, void *ws, hipSt
             stream ? launch(k_rmsnorm_adjoint<T, TPR, NV, true>) : launch(k_rmsnorm_adjoint<T, TPR, NV, false>);
             CHOL_LAUNCH_CHECK();
             if (blocks > 1) {
-                hipLaunchKernelGGL(k_sum_rows, dim3((unsigned)((a.cols + SUM_COLS - 1) / SUM_COLS)), dim3(SUM_COLS * SUM_PARTS), 0, st,
+                hipLaunchKernelGGL(k_sum_rows, dim3((unsigned)((a.cols + WAVE - 1) / WAVE)), dim3(1024), 0, st,
                                    (const float *)ws, (int)blocks, (int)a.cols, a.adj_w, a.accumulate);
                 CHOL_LAUNCH_CHECK();
             }

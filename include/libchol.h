@@ -450,7 +450,9 @@ chol_status chol_potrs_adjoint_batched(chol_dtype dtype, int64_t n, int64_t nrhs
  * The products of consecutive gates are formed in fp32: gates of magnitude at
  * most 1 are what the segmented form is meant for; where a run of larger ones
  * overflows, the result is inf or NaN.
- * batch * dim above 2^31 - 1 returns CHOL_ERR_NOT_SUPPORTED.
+ * The result does not depend on timing: equal calls give equal bits.
+ * batch * dim above 2^31 - 1, and sizes that need 2^32 threads or more, return
+ * CHOL_ERR_NOT_SUPPORTED.
  */
 chol_status chol_recurrence(chol_dtype dtype, int gate, int64_t batch, int64_t len, int64_t dim,
                             const void *a, int64_t lda, int64_t strideA,
@@ -514,7 +516,8 @@ chol_status chol_rmsnorm(chol_dtype dtype, int64_t rows, int64_t cols,
 
 /*
  * chol_rmsnorm_quant -- chol_rmsnorm with y in 8 bits (e4m3, largest value 448):
- *     scale = max |y| / 448 over a group,   q = e4m3(y / scale), to nearest even.
+ *     scale = max |y| / 448 over a group,   q = e4m3(y / scale), to nearest even
+ * (of a quotient that is right to half a step of fp32).
  *   group  columns that share a scale: 32, 64, 128 or 256 (the last group of a
  *          row may be shorter), or 0 for one scale a row.
  *   q      [out] device, one byte an element, leading dimension ldq.
@@ -573,7 +576,8 @@ chol_status chol_rmsnorm_adjoint_workspace_size(chol_dtype dtype, int64_t rows, 
  *           hash h, low half for m and high half for sqrt(v).
  *   master  nonzero: the tensors have fp32 master weights, which are read and
  *           updated, and p is written with their rounding; zero: p itself is.
- * State and weight arithmetic is fp32, each product and sum rounded by itself.
+ * State and weight arithmetic is fp32, each product, sum and root rounded by
+ * itself; the division of the update is within two steps.
  *   chunks, table   what chol_adamw_list gave; the table lies in device memory
  *           (8-byte aligned), copied there by the caller, and the tensors stay
  *           where they are for as long as it is used.
