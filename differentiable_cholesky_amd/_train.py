@@ -366,6 +366,8 @@ def chol_adamw_list(p, g, m, v, master=None, m_scale=None, v_scale=None, first=N
     p, g, m, v = list(p), list(g), list(m), list(v)
     if not p:
         raise ValueError("the list has no tensors")
+    if len(m) != len(p):
+        raise ValueError(f"m has {len(m)} tensors for {len(p)}")
     bits = {torch.float32: 32, torch.float8_e4m3fn: 8}.get(m[0].dtype)
     if bits is None:
         raise TypeError(f"states must be float32 or float8_e4m3fn, got {m[0].dtype}")
@@ -380,27 +382,32 @@ def chol_adamw_list(p, g, m, v, master=None, m_scale=None, v_scale=None, first=N
     for name, given in (("master", master), ("m_scale", m_scale), ("v_scale", v_scale)):
         if given is not None:
             columns[name] = (list(given), torch.float32)
-    items = (AdamwTensor * len(p))()
-    at = 0
     if first is not None:
         first = list(first)
         if len(first) != len(p):
             raise ValueError(f"first has {len(first)} entries for {len(p)} tensors")
+    device, sizes = p[0].device, [t.numel() for t in p]
+    tiles = [-(-n // ADAMW_TILE) for n in sizes]
     for name, (tensors, dtype) in columns.items():
         if len(tensors) != len(p):
             raise ValueError(f"{name} has {len(tensors)} tensors for {len(p)}")
+        counts = tiles if name.endswith("_scale") else sizes
         for i, t in enumerate(tensors):
-            n = p[i].numel()
-            _same(t, f"{name}[{i}]", p[0], t.shape, dtype)
-            if t.numel() != (-(-n // ADAMW_TILE) if name.endswith("_scale") else n):
-                raise ValueError(f"{name}[{i}] has {t.numel()} elements for {n} weights")
+            if t.dtype is not dtype or t.device != device:
+                _same(t, f"{name}[{i}]", p[0], t.shape, dtype)
+            if t.numel() != counts[i]:
+                raise ValueError(f"{name}[{i}] has {t.numel()} elements for {sizes[i]} weights")
             if not t.is_contiguous():
                 raise ValueError(f"{name}[{i}] must be contiguous")
-            setattr(items[i], name, t.data_ptr())
-    for i, t in enumerate(p):
-        items[i].n = t.numel()
-        items[i].first = at if first is None else first[i]
-        at += -(-t.numel() // ADAMW_TILE) * ADAMW_TILE
+    if first is None:
+        first, at = [], 0
+        for n in tiles:
+            first.append(at)
+            at += n * ADAMW_TILE
+    none = [None] * len(p)
+    pointers = [[t.data_ptr() for t in columns[k][0]] if k in columns else none
+                for k in ("p", "g", "m", "v", "master", "m_scale", "v_scale")]
+    items = (AdamwTensor * len(p))(*zip(*pointers, sizes, first))
     chunks, size = ctypes.c_int64(0), ctypes.c_size_t(0)
     _check(lib.chol_adamw_list(code, bits, len(p), items, None, 0, ctypes.byref(chunks), ctypes.byref(size)))
     host = torch.empty(max(size.value, 8), dtype=torch.uint8)

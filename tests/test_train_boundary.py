@@ -165,7 +165,7 @@ def test_norm_adjoint_workspace_size():
     for dt, width in ((BF16, 8), (F16, 8), (F32, 4)):
         for cols in (1, 64, 100, 128, 250, 300, 511, 512, 1000, 1024, 1025, 2000, 2047, 2048, 3000, 4096, 5000, 8192, 16384):
             vectors = -(-cols // width)
-            together = 1 if vectors > 128 else 256 // min(t for t in (8, 16, 32, 64) if t >= min(vectors, 64))
+            together = 1 if vectors > 256 else 256 // min(t for t in (8, 16, 32, 64) if t >= min(vectors, 64))
             assert size(dt, 1, cols) == size(dt, together, cols) == 0
             assert size(dt, together + 1, cols) == 2 * cols * 4
             assert size(dt, 1 << 20, cols) in (256 * cols * 4, 512 * cols * 4)
@@ -249,6 +249,8 @@ def test_adamw_binding_refuses():
         dc.chol_adamw_list(t, t, [x.half() for x in t], t)
     with pytest.raises(ValueError):
         dc.chol_adamw_list(t, t, t, t, m_scale=t)
+    with pytest.raises(ValueError):
+        dc.chol_adamw_list(t, t, [], t)
     e = [torch.zeros(8, dtype=torch.uint8).view(torch.float8_e4m3fn)]
     with pytest.raises(ValueError):
         dc.chol_adamw_list(t, t, e, e)
