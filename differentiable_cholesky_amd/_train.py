@@ -115,6 +115,8 @@ def _scratch(need: int, device, workspace):
 def _seq(t, name: str):
     """(pointer, ld, stride) of a [batch, len, dim] array with unit channel stride."""
     batch, length, dim = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), dim, length * dim
     sb, st, sc = t.stride()
     if dim > 1 and sc != 1:
         raise ValueError(f"{name} must have unit channel stride")

@@ -242,3 +242,26 @@ def test_captured_into_a_graph():
         for k in a:
             for x, y in zip(a[k], b[k]):
                 assert torch.equal(x.float(), y.float()), k
+
+
+def test_a_list_longer_than_one_launch_takes():
+    """2^21 chunks of 4096 weights and a few more: the last ones are stepped as a list of their own is."""
+    import differentiable_cholesky_amd as dc
+    big, tail = (1 << 21) * 4096, 5000
+    dev = dict(device="cuda")
+    p, g = (torch.zeros(big + tail, dtype=torch.bfloat16, **dev) for _ in range(2))
+    m, v = (torch.zeros(big + tail, dtype=torch.uint8, **dev).view(E4M3) for _ in range(2))
+    scales = [torch.ones(-(-(big + tail) // TILE), **dev) for _ in range(2)]
+    p[big:].normal_()
+    g[big:].normal_()
+    own = [t[big:].clone() for t in (p, g)] + [torch.zeros(tail, dtype=torch.uint8, **dev).view(E4M3) for _ in range(2)]
+    own_scales = [torch.ones(-(-tail // TILE), **dev) for _ in range(2)]
+    dc.chol_adamw(dc.chol_adamw_list([p], [g], [m], [v], m_scale=[scales[0]], v_scale=[scales[1]]), seed=5, **HYPER)
+    dc.chol_adamw(dc.chol_adamw_list([own[0]], [own[1]], [own[2]], [own[3]], m_scale=[own_scales[0]],
+                                     v_scale=[own_scales[1]], first=[big]), seed=5, **HYPER)
+    assert not torch.equal(own[0], torch.zeros_like(own[0])) and torch.equal(p[big:], own[0])
+    for x, y in ((m, own[2]), (v, own[3])):
+        assert torch.equal(x[big:].view(torch.uint8), y.view(torch.uint8))
+    for x, y in zip(scales, own_scales):
+        assert torch.equal(x[big // TILE:], y)
+    assert not p[big - 100000:big].any()

@@ -214,3 +214,25 @@ def test_equal_calls_give_equal_bits(dtype):
         assert torch.equal(again[0], h) and torch.equal(again[1], last), k
         for x, y in zip(dc.chol_recurrence_adjoint(a, h, adj, h0=h0, adjHlast=adj_last, gate="log"), grads):
             assert torch.equal(x, y), k
+
+
+def test_more_elements_than_32_bits_count():
+    import differentiable_cholesky_amd as dc
+    length, dim, tail = 70001, 32768, 8                       # 2.3e9 elements
+    g = torch.Generator(device="cuda").manual_seed(12)
+    a = torch.empty(1, length, dim, dtype=torch.bfloat16, device="cuda").uniform_(0.5, 0.99, generator=g)
+    b = torch.empty_like(a).uniform_(-1, 1, generator=g)
+    h, last = dc.chol_recurrence(a, b)
+    cut = slice(dim - tail, dim)
+    h1, last1 = dc.chol_recurrence(a[..., cut], b[..., cut])
+    assert torch.equal(h[..., cut], h1) and torch.equal(last[:, cut], last1)
+    adj = b[0, -50:, cut].double()
+    da, db, _ = dc.chol_recurrence_adjoint(a, h, b, adjB=b)
+    for t in range(length - 50, length):
+        want = db[0, t, cut].double() * h[0, t - 1, cut].double()
+        # adjB is lam rounded once, and adjA rounds its product with lam once
+        assert ((da[0, t, cut].double() - want).abs() <= 2.02 * tu.HALF[torch.bfloat16] * want.abs() + 1e-30).all(), t
+        if t + 1 < length:
+            after = a[0, t + 1, cut].double() * db[0, t + 1, cut].double()
+            lam = adj[t - length + 50] + after
+            assert ((db[0, t, cut].double() - lam).abs() <= 1.01 * tu.HALF[torch.bfloat16] * (lam.abs() + after.abs())).all()

@@ -237,3 +237,19 @@ def test_rows_beyond_the_caches():
         q1, s1, _ = dc.chol_rmsnorm_quant(x[part], w, residual=r[part], group=64)
         assert torch.equal(q1.float(), q[part].float()) and torch.equal(s1, scale[part])
         assert torch.equal(dc.chol_rmsnorm_adjoint(h1, w, adj[part], adjH=adj_h[part])[0], dx[part])
+
+
+def test_more_elements_than_32_bits_count():
+    import differentiable_cholesky_amd as dc
+    rows, cols = 1100000, 2048                                # 2.3e9 elements
+    g = torch.Generator(device="cuda").manual_seed(10)
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w = torch.empty(cols, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    part = x[-100:].clone()
+    q, scale, _ = dc.chol_rmsnorm_quant(x, w, group=64)
+    q1, s1, _ = dc.chol_rmsnorm_quant(part, w, group=64)
+    assert torch.equal(q[-100:].float(), q1.float()) and torch.equal(scale[-100:], s1)
+    y, _ = dc.chol_rmsnorm(x, w)
+    assert torch.equal(y[-100:], dc.chol_rmsnorm(part, w)[0])
+    dx, _ = dc.chol_rmsnorm_adjoint(x, w, y, adjX=y)
+    assert torch.equal(dx[-100:], dc.chol_rmsnorm_adjoint(part, w, dc.chol_rmsnorm(part, w)[0])[0])
