@@ -8,9 +8,9 @@
 //
 // One pass over memory: a lane holds R consecutive steps of one 32-bit word of
 // channels (two 16-bit ones, or an fp32 one) in registers, composes them, and
-// walks them again from registers once it knows the state before them.  Waves
-// of a workgroup lie along the steps (`waves`, fewer for short sequences) and
-// across channels, and exchange their (P, Q) through LDS.  Workgroups of one
+// walks them again from registers once it knows the state before them.  Teams of
+// lanes (waves, or parts of them for few channels) lie along the steps (`teams`,
+// fewer for short sequences) and across channels, and exchange their (P, Q) through LDS.  Workgroups of one
 // channel group form a chain along the sequence, cut into groups of LINKS: a
 // workgroup composes what those before it in its group published, and applies
 // that to the state its group starts from, which the last workgroup of the group
@@ -32,7 +32,8 @@ namespace chol {
 
 namespace {
 
-constexpr int WAVE = 64, WAVES = 8, THREADS = WAVE * WAVES;
+constexpr int WAVE = 64, THREADS = 512;
+constexpr int NARROW = 16; // lanes of a part of a wave
 constexpr int LINKS = 8, WINDOW = 4; // workgroups of a chain's group; words read at once
 
 template <typename T> constexpr int word_channels = 4 / (int)sizeof(T);
@@ -123,7 +124,8 @@ template <typename T, bool LOG> __device__ __forceinline__ float gate(float x)
 }
 
 struct Plan {
-    int waves;          // of a workgroup along the steps; the others lie across channels
+    int lanes;          // of a team: a wave, or a part of one for few channels
+    int teams;          // of a workgroup along the steps; the others lie across channels
     int steps;          // R
     int chunks, groups; // workgroups along the steps, and across a batch element's channels
 };
@@ -168,15 +170,16 @@ __global__ void __launch_bounds__(256) k_rec_clear(word_pair *ws, int64_t pairs)
 
 // (four waves a SIMD, so two workgroups a CU: without it the partial words' loads
 // take the registers of one, adjoint of 1 x 65536 x 2048 bf16 256 -> 311 us)
-template <typename T, bool LOG, bool ADJ, int R>
+template <typename T, bool LOG, bool ADJ, int R, int LANES>
 __global__ void __launch_bounds__(THREADS, 4) k_recurrence(RecArgs r, Plan p, uint64_t *ws)
 {
-    constexpr int V = word_channels<T>, SPAN = WAVE * V;
-    __shared__ float2 s_link[WAVES][SPAN];
-    __shared__ float s_in[WAVES][SPAN];
+    constexpr int V = word_channels<T>, SPAN = LANES * V, TEAMS = THREADS / LANES;
+    __shared__ float2 s_link[TEAMS][SPAN];
+    __shared__ float s_in[TEAMS][SPAN];
     __shared__ unsigned s_ticket;
-    const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int jw = wave % p.waves, cw = wave / p.waves, across = WAVES / p.waves;
+    const int lane = threadIdx.x % LANES;
+    const int team = LANES < WAVE ? threadIdx.x / LANES : __builtin_amdgcn_readfirstlane(threadIdx.x / LANES);
+    const int jw = team % p.teams, cw = team / p.teams, across = TEAMS / p.teams;
     unsigned block = blockIdx.x;
     if (p.chunks > 1) {
         // chains advance in the order in which workgroups start: whatever a
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_recurrence(RecArgs r, Plan p, ui
     const unsigned chunk = block / chains, chain = block % chains;
     const int64_t z = chain / p.groups;
     const int64_t c0 = ((int64_t)(chain % p.groups) * across + cw) * SPAN, c = c0 + lane * V;
-    const int64_t s0 = ((int64_t)chunk * p.waves + jw) * R;
+    const int64_t s0 = ((int64_t)chunk * p.teams + jw) * R;
     // walk step s is row s, or counted from the end
     const auto row = [&](int64_t s) { return ADJ ? r.len - 1 - s : s; };
     const T *pa = (const T *)r.a.p + z * r.a.stride + c0, *pb = (const T *)r.b.p + z * r.b.stride + c0;
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_recurrence(RecArgs r, Plan p, ui
     const auto state = [&](const float *x, int v) { return x && c + v < r.dim ? x[z * r.dim + c + v] : 0.f; };
 
     float x[V];
-    if (p.waves * p.chunks == 1) {
+    if (p.teams * p.chunks == 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
             x[v] = state(r.start, v);
@@ -253,14 +256,14 @@ __global__ void __launch_bounds__(THREADS, 4) k_recurrence(RecArgs r, Plan p, ui
                 Q[v] = ADJ ? g * (Q[v] + y) : fmaf(g, Q[v], y);
                 P[v] *= g;
             }
-            s_link[wave][lane * V + v] = make_float2(P[v], Q[v]);
+            s_link[team][lane * V + v] = make_float2(P[v], Q[v]);
         }
         __syncthreads();
         if (jw == 0) {
-            for (int k = 1; k < p.waves; ++k)
+            for (int k = 1; k < p.teams; ++k)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float2 n = s_link[wave + k][lane * V + v];
+                    const float2 n = s_link[team + k][lane * V + v];
                     Q[v] = fmaf(n.x, Q[v], n.y);
                     P[v] *= n.x;
                 }
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_recurrence(RecArgs r, Plan p, ui
             for (int k = 0; k < jw; ++k)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float2 n = s_link[wave - jw + k][lane * V + v];
+                    const float2 n = s_link[team - jw + k][lane * V + v];
                     x[v] = fmaf(n.x, x[v], n.y);
                 }
         }
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_recurrence(RecArgs r, Plan p, ui
                 store_part(d, c, r.dim, pack<T>(da));
         }
     }
-    if (chunk == (unsigned)p.chunks - 1 && jw == p.waves - 1)
+    if (chunk == (unsigned)p.chunks - 1 && jw == p.teams - 1)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (c + v < r.dim)
@@ -386,13 +389,22 @@ constexpr int SHORT = 8, LONG = 32, LONG_ADJOINT = 20; // R
 
 Plan plan_of(chol_dtype dt, bool adjoint, int64_t batch, int64_t len, int64_t dim)
 {
-    const int64_t span = WAVE * (4 / (int64_t)lowp_size(dt));
+    // Few channels leave most of a wave without work: quarters of waves walk runs of
+    // their own then (us forward and adjoint, bf16: 16 x 65536 x 16 142 and 247 with
+    // waves, 77 and 122 with quarters; 16 x 30000 x 64 101 and 162, 61 and 98; x 96
+    // 125 and 196, 85 and 135).  Not where a row would end inside a second quarter,
+    // which then shares the row's cache lines: 8 x 20000 x 30 fp32 30 and 42, 40 and 45.
+    const int64_t words = (dim * (int64_t)lowp_size(dt) + 3) / 4;
+    const bool quarters = words <= NARROW || (words < WAVE && words % NARROW == 0);
+    const int lanes = quarters ? NARROW : WAVE, all = THREADS / lanes;
+    const int64_t span = lanes * (4 / (int64_t)lowp_size(dt));
     const auto with = [&](int steps) {
         Plan p;
+        p.lanes = lanes;
         p.steps = steps;
-        p.waves = ceil_pow2((len + steps - 1) / steps, WAVES);
-        p.chunks = (int)std::max<int64_t>(1, (len + p.waves * steps - 1) / (p.waves * steps));
-        const int64_t width = span * (WAVES / p.waves);
+        p.teams = ceil_pow2((len + steps - 1) / steps, all);
+        p.chunks = (int)std::max<int64_t>(1, (len + p.teams * steps - 1) / (p.teams * steps));
+        const int64_t width = span * (all / p.teams);
         p.groups = (int)((dim + width - 1) / width);
         return p;
     };
@@ -401,31 +413,34 @@ Plan plan_of(chol_dtype dt, bool adjoint, int64_t batch, int64_t len, int64_t di
     // CU (40 and more: 8 x 4096 x 2048 97 us, with 32 86).  Where one workgroup
     // holds the sequence with 8 there are no links, and the lanes' runs count:
     // 64 x 16 x 2048 bf16 forward 8.8 us with 8, 11.3 with 32; adjoint 13.3, 17.7.
-    return with(len <= 1 ? 1 : len <= WAVES * SHORT ? SHORT : adjoint ? LONG_ADJOINT : LONG);
+    return with(len <= 1 ? 1 : len <= all * SHORT ? SHORT : adjoint ? LONG_ADJOINT : LONG);
 }
 
 int64_t links_of(chol_dtype dt, const Plan &p, int64_t batch)
 {
-    return p.chunks > 1 ? batch * p.groups * p.chunks * WAVE * (4 / (int64_t)lowp_size(dt)) * (WAVES / p.waves) : 0;
+    return p.chunks > 1 ? batch * p.groups * p.chunks * (4 / (int64_t)lowp_size(dt)) * (THREADS / p.teams) : 0;
 }
 
 template <typename T, bool LOG, bool ADJ> chol_status run(chol_dtype dt, const RecArgs &r, void *ws, hipStream_t st)
 {
     const Plan p = plan_of(dt, ADJ, r.batch, r.len, r.dim);
     if (p.chunks > 1) {
-        const int64_t pairs = links_of(dt, p, r.batch) / 2 + 1; // (a row of links is a multiple of 64)
+        const int64_t pairs = links_of(dt, p, r.batch) / 2 + 1; // (a row of links is a multiple of 16)
         hipLaunchKernelGGL(k_rec_clear, dim3((unsigned)((pairs + 256 * CLEAR - 1) / (256 * CLEAR))), dim3(256), 0, st,
                            (word_pair *)ws, pairs);
         CHOL_LAUNCH_CHECK();
     }
     const dim3 grid((unsigned)(r.batch * p.groups * p.chunks));
     constexpr int L = ADJ ? LONG_ADJOINT : LONG;
-    if (p.steps == 1)
-        hipLaunchKernelGGL((k_recurrence<T, LOG, ADJ, 1>), grid, dim3(THREADS), 0, st, r, p, (uint64_t *)ws);
-    else if (p.steps == SHORT)
-        hipLaunchKernelGGL((k_recurrence<T, LOG, ADJ, SHORT>), grid, dim3(THREADS), 0, st, r, p, (uint64_t *)ws);
+    const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, st, r, p, (uint64_t *)ws); };
+    if (p.lanes == WAVE)
+        p.steps == 1       ? launch(k_recurrence<T, LOG, ADJ, 1, WAVE>)
+        : p.steps == SHORT ? launch(k_recurrence<T, LOG, ADJ, SHORT, WAVE>)
+                           : launch(k_recurrence<T, LOG, ADJ, L, WAVE>);
     else
-        hipLaunchKernelGGL((k_recurrence<T, LOG, ADJ, L>), grid, dim3(THREADS), 0, st, r, p, (uint64_t *)ws);
+        p.steps == 1       ? launch(k_recurrence<T, LOG, ADJ, 1, NARROW>)
+        : p.steps == SHORT ? launch(k_recurrence<T, LOG, ADJ, SHORT, NARROW>)
+                           : launch(k_recurrence<T, LOG, ADJ, L, NARROW>);
     CHOL_LAUNCH_CHECK();
     return CHOL_OK;
 }

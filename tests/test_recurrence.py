@@ -37,7 +37,7 @@ def check_adjoint(a, h, adj, h0, adj_last, gate, got, what):
 
 
 SIZES = [(1, 1, 1), (2, 1, 5), (1, 2, 64), (3, 15, 65), (2, 16, 128), (1, 17, 130), (2, 127, 33), (1, 129, 256), (5, 300, 7),
-         (1, 1025, 100), (2, 2049, 66), (1, 5000, 31)]
+         (1, 1025, 100), (2, 2049, 66), (1, 5000, 31), (2, 3000, 16), (1, 2100, 32), (3, 700, 64), (1, 9000, 3), (9, 257, 17)]
 
 
 @pytest.mark.parametrize("gate", ["linear", "log"])
