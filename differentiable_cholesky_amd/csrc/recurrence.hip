@@ -14,7 +14,7 @@
 // channel group form a chain along the sequence, cut into groups of LINKS: a
 // workgroup composes what those before it in its group published, and applies
 // that to the state its group starts from, which the last workgroup of the group
-// before published.  So the chain waits once a group, every sum is formed in
+// before published (links.hpp).  So the chain waits once a group, every sum is formed in
 // one order whatever the workgroups' timing, and equal calls give equal bits.
 //
 // Every element is read once and written once and costs a few operations, so
@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "links.hpp"
 #include "lowp.hpp"
 #include "recurrence.hpp"
 
@@ -34,7 +35,6 @@ namespace {
 
 constexpr int WAVE = 64, THREADS = 512;
 constexpr int NARROW = 16; // lanes of a part of a wave
-constexpr int LINKS = 8, WINDOW = 4; // workgroups of a chain's group; words read at once
 
 template <typename T> constexpr int word_channels = 4 / (int)sizeof(T);
 
@@ -130,9 +130,8 @@ struct Plan {
     int chunks, groups; // workgroups along the steps, and across a batch element's channels
 };
 
-// What a workgroup publishes, one 64-bit word a channel, written once and read
-// whole, so that no flag or fence is needed: the (P, Q) of its steps, or, from
-// the last of a group, the state after it in Q.  The workspace is filled with
+// What a workgroup publishes (links.hpp), one 64-bit word a channel, written once and
+// read whole, so that no flag or fence is needed: P and Q.  The workspace is filled with
 // EMPTY first (P's NaN of all ones, which a published P never is).
 constexpr uint64_t EMPTY = ~(uint64_t)0;
 
@@ -154,6 +153,19 @@ __device__ __forceinline__ float2 arrived(const uint64_t *p, uint64_t w)
     }
     return make_float2(__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32)));
 }
+
+// A lane's view of its chain (links.hpp): its word of workgroup k lies k * stride on.
+template <typename State> struct Words {
+    uint64_t *links;
+    int64_t stride;
+    const float *from;
+    const State &state;
+    __device__ __forceinline__ float start(int v) const { return state(from, v); }
+    __device__ __forceinline__ uint64_t *at(unsigned k, int v) const { return links + (int64_t)k * stride + v; }
+    __device__ __forceinline__ void publish(unsigned k, int v, float P, float Q) const { chol::publish(at(k, v), P, Q); }
+    __device__ __forceinline__ uint64_t peek(unsigned k, int v) const { return chol::peek(at(k, v)); }
+    __device__ __forceinline__ float2 arrived(unsigned k, int v, uint64_t w) const { return chol::arrived(at(k, v), w); }
+};
 
 // Fills the workspace, two words a store; the first two are the tickets'.
 constexpr int CLEAR = 4; // stores of a thread
@@ -270,45 +282,8 @@ __global__ void __launch_bounds__(THREADS, 4) k_recurrence(RecArgs r, Plan p, ui
             if (p.chunks > 1) {
                 const int64_t stride = (int64_t)across * SPAN;
                 uint64_t *const links = ws + 2 + (int64_t)chain * p.chunks * stride + cw * SPAN + lane * V;
-                const auto link = [&](unsigned at, int v) { return links + (int64_t)at * stride + v; };
-                const unsigned first = chunk / LINKS * LINKS;
-                const bool last = chunk % LINKS == LINKS - 1, read = chunk + 1 < (unsigned)p.chunks;
-                if (!last && read)
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        publish(link(chunk, v), P[v], Q[v]);
-                float bp[V], bq[V]; // of the group's workgroups before this one
-                uint64_t base[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    bp[v] = 1.f, bq[v] = 0.f;
-                    base[v] = first ? peek(link(first - 1, v)) : 0;
-                }
-                for (unsigned at = first; at < chunk; at += WINDOW) {
-                    uint64_t w[WINDOW][V];
-#pragma unroll
-                    for (int k = 0; k < WINDOW; ++k)
-#pragma unroll
-                        for (int v = 0; v < V; ++v)
-                            if (at + k < chunk)
-                                w[k][v] = peek(link(at + k, v));
-#pragma unroll
-                    for (int k = 0; k < WINDOW; ++k)
-#pragma unroll
-                        for (int v = 0; v < V; ++v)
-                            if (at + k < chunk) {
-                                const float2 n = arrived(link(at + k, v), w[k][v]);
-                                bq[v] = fmaf(n.x, bq[v], n.y);
-                                bp[v] *= n.x;
-                            }
-                }
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float from = first ? arrived(link(first - 1, v), base[v]).y : state(r.start, v);
-                    x[v] = chunk == first ? from : fmaf(bp[v], from, bq[v]);
-                    if (last && read)
-                        publish(link(chunk, v), 0.f, fmaf(P[v], x[v], Q[v]));
-                }
+                Words<decltype(state)> words{links, stride, r.start, state};
+                state_before(words, chunk, (unsigned)p.chunks, P, Q, x);
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
