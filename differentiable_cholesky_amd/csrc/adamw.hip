@@ -182,10 +182,20 @@ __device__ __forceinline__ void write_codes(void *base, float *scale, uint32_t a
     for (int k = 0; k < V; ++k)
         most = max(most, __float_as_uint(x[k]) & 0x7fffffffu);
     most = wave_max(most);
+    const bool finite = most < 0x7f800000u; // the same for the whole wave
+    if (!finite) { // the scale is that of the finite values: the others have no part in their neighbours' codes
+        most = 0;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const unsigned mag = __float_as_uint(x[k]) & 0x7fffffffu;
+            most = max(most, mag < 0x7f800000u ? mag : 0u);
+        }
+        most = wave_max(most);
+    }
     const int e = max((int)(most >> 23) - 7, 1);
     const float inv = __uint_as_float((unsigned)(254 - e) << 23);
     unsigned u = 0;
-    if (most < 0x7f800000u) { // the same for the whole wave
+    if (finite) {
 #pragma unroll
         for (int k = 0; k < V; ++k)
             u |= code_of(x[k] * inv, noise[k], keep) << (8 * k);

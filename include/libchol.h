@@ -569,7 +569,8 @@ chol_status chol_rmsnorm_adjoint_workspace_size(chol_dtype dtype, int64_t rows, 
  *   bits    32: m and v are fp32.  8: m and sqrt(v) are e4m3 codes, the element
  *           a code times its tile's scale; a tile is 256 elements of one tensor
  *           (the last may be shorter).  Scales are powers of two that bring the
- *           tile's largest element into [2^7, 2^8), but at least 2^-126.  A code is rounded up in
+ *           tile's largest finite element into [2^7, 2^8), but at least 2^-126; an infinite or
+ *           NaN element has the code NaN and leaves the others as they are.  A code is rounded up in
  *           magnitude where 16 random bits and the dropped part carry; a nonzero
  *           sqrt(v) is never stored as zero.  The random bits of the element at
  *           position k of the list are those of (k + h(seed)) mod 2^32 under an integer

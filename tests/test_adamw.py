@@ -265,3 +265,37 @@ def test_a_list_longer_than_one_launch_takes():
     for x, y in zip(scales, own_scales):
         assert torch.equal(x[big // TILE:], y)
     assert not p[big - 100000:big].any()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_non_finite_gradient_stays_in_its_element(bad, bits):
+    """Steps after it: every other weight and state is what it is where that element's gradient is zero, which adds
+    nothing to its tile; a tile of non-finite elements only, and one at the ragged end, among them."""
+    import differentiable_cholesky_amd as dc
+    n, hit = 1000, torch.zeros(1000, dtype=torch.bool)
+    hit[[3, 700, 999]] = True
+    hit[256:512] = True
+    before = make(torch.float32, False, bits, seed=9, sizes=[n])
+    for k in ("m", "v"):
+        raw = before[k][0].view(torch.uint8) if bits == 8 else before[k][0]
+        raw[hit] = 0
+    runs = []
+    for value in (0.0, bad):
+        t, _ = on_gpu(before)
+        handle = dc.chol_adamw_list(t["p"], t["g"], t["m"], t["v"], m_scale=t.get("m_scale"), v_scale=t.get("v_scale"))
+        g = torch.Generator().manual_seed(10)
+        for step in range(1, 7):
+            grad = 1e-2 * torch.randn(n, generator=g)
+            grad[hit] = value if step == 2 else 0.0
+            t["g"][0].copy_(grad)
+            dc.chol_adamw(handle, seed=step, **dict(HYPER, step=step))
+        runs.append(t)
+    rest = ~hit.cuda()
+    for k in ("p", "m", "v"):
+        x, y = (t[k][0].float() for t in runs)
+        assert torch.isfinite(x).all() and torch.equal(y[rest], x[rest]), k
+        assert not torch.isfinite(y[~rest]).any(), k
+    if bits == 8:
+        for k in ("m_scale", "v_scale"):
+            assert torch.equal(runs[0][k][0], runs[1][k][0]), k
