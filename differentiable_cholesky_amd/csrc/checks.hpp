@@ -33,11 +33,21 @@ inline bool rect_alias_ok(const void *i, int64_t ldi, int64_t si, const void *o,
     return !overlap(rect_extent(i, rows, cols, ldi, batch, si, es), rect_extent(o, rows, cols, ldo, batch, so, es));
 }
 
+// Whether a batch of rows x cols blocks spans few enough elements that products of
+// its sizes and their bytes stay inside 64 bits (no array is larger).
+inline bool span_ok(int64_t rows, int64_t cols, int64_t ld, int64_t batch, int64_t stride)
+{
+    const __int128 most = (__int128)1 << 59;
+    const __int128 r = rows > 1 ? (__int128)(rows - 1) * ld : 0, b = batch > 1 ? (__int128)(batch - 1) * stride : 0;
+    return r <= most && b <= most && r + b + cols <= most;
+}
+
 // A batch of rows x cols blocks that no element belongs to twice: the batch
 // outside the rows, or (sequence-major storage) the rows outside the batch.
 inline bool layout_ok(int64_t rows, int64_t cols, int64_t ld, int64_t batch, int64_t stride)
 {
-    if ((rows > 1 && ld < cols) || (batch > 1 && stride < cols) || ld < 0 || stride < 0)
+    if ((rows > 1 && ld < cols) || (batch > 1 && stride < cols) || ld < 0 || stride < 0 ||
+        !span_ok(rows, cols, ld, batch, stride))
         return false;
     return rows <= 1 || batch <= 1 || stride >= ld * (rows - 1) + cols || ld >= stride * (batch - 1) + cols;
 }

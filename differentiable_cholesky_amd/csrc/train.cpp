@@ -21,10 +21,8 @@ using namespace chol;
 
 namespace {
 
-// Sizes whose products stay far inside 64 bits.
+// Most elements of a tensor, and of the distance between two rows.
 const int64_t MAX_EXTENT = (int64_t)1 << 40;
-
-bool size_ok(int64_t n) { return n >= 0 && n <= MAX_EXTENT; }
 
 } // namespace
 
@@ -192,7 +190,10 @@ chol_status norm_sizes(chol_dtype dt, int64_t rows, int64_t cols)
     return CHOL_OK;
 }
 
-bool rows_ok(const Rows2 &a, int64_t rows) { return a.p && a.ld <= MAX_EXTENT && (rows <= 1 ? a.ld >= 0 : a.ld >= a.cols); }
+bool rows_ok(const Rows2 &a, int64_t rows)
+{
+    return a.p && a.ld <= MAX_EXTENT && (rows <= 1 ? a.ld >= 0 : a.ld >= a.cols) && span_ok(rows, a.cols, a.ld, 1, 0);
+}
 
 // A row is read whole before any of it is written, by the threads that read
 // it: an output may be an input itself.

@@ -88,6 +88,17 @@ def test_recurrence_adjoint_refusals(change):
     assert adjoint(**change) == INVALID
 
 
+@pytest.mark.parametrize("length,ld", [((1 << 24) + 1, 1 << 40), ((1 << 31) - 1, 1 << 40), ((1 << 22) + 1, 1 << 40)])
+def test_spans_beyond_64_bits_are_refused(length, ld):
+    """Rows of ld elements whose byte offsets pass 64 bits; 2^24 of 2^40 come out as no offset at all."""
+    rows = dict(batch=1, length=length, dim=1, a=(P[0], 1, 0), b=(P[1], 1, 0), h=(P[4], 1, 0))
+    assert forward(**dict(rows, h=(P[1], ld, 0))) == INVALID
+    assert forward(**dict(rows, a=(P[0], ld, 0), b=(P[1], ld, 0), h=(P[0] + (1 << 20), ld, 0))) == INVALID
+    assert forward(**dict(rows, batch=2, length=3, a=(P[0], 1, ld), b=(P[1], 1, ld), h=(P[0] + 64, 1, ld * 2))) == INVALID
+    assert norm(rows=length, x=(P[0], ld), r=(None, 0), y=(P[0] + (1 << 20), ld)) == INVALID
+    assert norm_adjoint(rows=length, h=(P[0], ld), dx=(P[0] + (1 << 20), ld)) == INVALID
+
+
 def test_binding_refuses():
     a = torch.zeros(2, 3, 4)
     with pytest.raises(ValueError):
