@@ -35,7 +35,7 @@ chol_status chol_recurrence_workspace_size(chol_dtype dt, int64_t batch, int64_t
     if (!bytes || !lowp_dtype(dt) || batch < 0 || len < 0 || dim < 0)
         return CHOL_ERR_INVALID_VALUE;
     *bytes = 0;
-    if (batch == 0 || len == 0 || dim == 0)
+    if (batch == 0 || dim == 0)
         return CHOL_OK;
     if (batch > INT32_MAX || len > INT32_MAX || dim > INT32_MAX || batch * dim > INT32_MAX)
         return CHOL_ERR_NOT_SUPPORTED;

@@ -88,6 +88,17 @@ def test_recurrence_adjoint_refusals(change):
     assert adjoint(**change) == INVALID
 
 
+def test_an_empty_sequence_has_the_limits_of_one_step():
+    """It copies the states, with as many threads."""
+    none = (None, 0, 0)
+    for batch, dim in ((1 << 24, 1), (1 << 20, 1 << 20), (1 << 31, 1)):
+        assert need(BF16, batch, 0, dim)[0] == need(BF16, batch, 1, dim)[0] == NOTSUP
+        assert forward(batch=batch, length=0, dim=dim, a=none, b=none, h=none) == NOTSUP
+        assert adjoint(batch=batch, length=0, dim=dim, a=none, h=none, adj=none, da=none, db=none) == NOTSUP
+    assert need(BF16, 1 << 22, 0, 16) == (OK, 0)
+    assert forward(length=0, a=none, b=none, h=none, last=None) == INVALID
+
+
 @pytest.mark.parametrize("length,ld", [((1 << 24) + 1, 1 << 40), ((1 << 31) - 1, 1 << 40), ((1 << 22) + 1, 1 << 40)])
 def test_spans_beyond_64_bits_are_refused(length, ld):
     """Rows of ld elements whose byte offsets pass 64 bits; 2^24 of 2^40 come out as no offset at all."""
