@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cstddef>
 #include <cstdint>
+#include <utility>
 
 namespace chol {
 
@@ -52,21 +53,37 @@ inline bool layout_ok(int64_t rows, int64_t cols, int64_t ld, int64_t batch, int
     return rows <= 1 || batch <= 1 || stride >= ld * (rows - 1) + cols || ld >= stride * (batch - 1) + cols;
 }
 
-// Whether two such batches share no element.  Blocks whose address ranges
-// interleave (column slices of one joint buffer) are apart if their columns
-// are, counted modulo a row length that both share.
+// Whether two such batches of the same sizes share no element.  Blocks whose address
+// ranges interleave (column slices of one joint buffer) are compared where both have
+// the same distances: elements a apart in one coordinate and b in the other lie
+// a * outer + b * inner + columns apart, and what the inner ones reach is less than
+// `outer`, so two values of each count.
 inline bool apart(const void *p, int64_t ldp, int64_t sp, const void *q, int64_t ldq, int64_t sq, int64_t rows,
                   int64_t cols, int64_t batch, size_t es)
 {
     if (!overlap(rect_extent(p, rows, cols, ldp, batch, sp, es), rect_extent(q, rows, cols, ldq, batch, sq, es)))
         return true;
-    // the period of the rows' addresses: the row length, or the batch's where there is one row
-    const int64_t period = rows > 1 ? ldp : sp;
-    if (ldp != ldq || sp != sq || period <= 0 || (batch > 1 && sp % period != 0))
+    if ((rows > 1 && ldp != ldq) || (batch > 1 && sp != sq))
         return false;
-    const uintptr_t d = (uintptr_t)p > (uintptr_t)q ? (uintptr_t)p - (uintptr_t)q : (uintptr_t)q - (uintptr_t)p;
-    const int64_t r = (int64_t)(d / es % (uintptr_t)period);
-    return d % es == 0 && r >= cols && r + cols <= period;
+    const uintptr_t bytes = (uintptr_t)p > (uintptr_t)q ? (uintptr_t)p - (uintptr_t)q : (uintptr_t)q - (uintptr_t)p;
+    if (bytes % es != 0)
+        return false;
+    // (a coordinate of one value has no distance: one that nothing reaches stands for it)
+    const int64_t none = (int64_t)1 << 60;
+    int64_t inner = rows > 1 ? ldp : none, outer = batch > 1 ? sp : none;
+    int64_t inners = rows, outers = batch;
+    if (inner > outer) {
+        std::swap(inner, outer);
+        std::swap(inners, outers);
+    }
+    const int64_t d = (int64_t)(bytes / es);
+    for (int64_t i = d / outer; i <= d / outer + 1 && i < outers; ++i) {
+        const int64_t left = d > i * outer ? d - i * outer : i * outer - d;
+        for (int64_t j = left / inner; j <= left / inner + 1 && j < inners; ++j)
+            if (left - j * inner > -cols && left - j * inner < cols)
+                return false;
+    }
+    return true;
 }
 
 // An output over an input: exactly the same elements, or none in common.

@@ -236,3 +236,35 @@ def test_more_elements_than_32_bits_count():
             after = a[0, t + 1, cut].double() * db[0, t + 1, cut].double()
             lam = adj[t - length + 50] + after
             assert ((db[0, t, cut].double() - lam).abs() <= 1.01 * tu.HALF[torch.bfloat16] * (lam.abs() + after.abs())).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("length", [1, 70, 1500])
+def test_joint_buffers_in_either_order(dtype, length):
+    """a and h, then adjA and adjB, as column slices of one buffer: sequence-major, and batch elements padded by less
+    than a row."""
+    import differentiable_cholesky_amd as dc
+    batch, dim = 3, 67
+    a, b, adj, h0, adj_last = make(batch, length, dim, dtype, "log", True, seed=13)
+    h, last = dc.chol_recurrence(a, b, h0=h0, gate="log")
+    grads = dc.chol_recurrence_adjoint(a, h, adj, h0=h0, adjHlast=adj_last, gate="log")
+
+    def joint(major):
+        wide = 2 * dim + 3
+        if major:
+            return torch.full((length, batch, wide), 7.0, dtype=dtype, device="cuda").transpose(0, 1)
+        flat = torch.full((batch * (length * wide + 5),), 7.0, dtype=dtype, device="cuda")
+        return flat.as_strided((batch, length, wide), (length * wide + 5, wide, 1))
+
+    for major in (True, False):
+        x, y = joint(major), joint(major)
+        one, other = slice(1, 1 + dim), slice(1 + dim, 1 + 2 * dim)
+        x[..., one].copy_(a)
+        got, end = dc.chol_recurrence(x[..., one], b, h0=h0, h=x[..., other], gate="log")
+        assert torch.equal(got, h) and torch.equal(end, last) and torch.equal(x[..., one], a)
+        back = dc.chol_recurrence_adjoint(x[..., one], x[..., other], adj, h0=h0, adjHlast=adj_last, adjA=y[..., one],
+                                          adjB=y[..., other], gate="log")
+        for p, q in zip(back, grads):
+            assert torch.equal(p, q)
+        for t in (x, y):
+            assert (t[..., 0] == 7).all() and (t[..., 1 + 2 * dim:] == 7).all()

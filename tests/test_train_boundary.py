@@ -88,6 +88,48 @@ def test_recurrence_adjoint_refusals(change):
     assert adjoint(**change) == INVALID
 
 
+def shared(length, dim, batch, ld, stride, d):
+    """Whether two such arrays, d elements apart, have an element in common."""
+    import numpy as np
+    one = (np.arange(batch)[:, None, None] * stride + np.arange(length)[:, None] * ld + np.arange(dim)).ravel()
+    return bool(np.isin(one, one + d).any())
+
+
+def test_slices_of_one_buffer_are_apart_where_no_element_is_shared():
+    """Two arrays with the same distances, at every kind of offset, against the sets of their elements.  The missing
+    workspace is found after the arrays have been compared."""
+    import random
+    rng = random.Random(0)
+    seen = {False: 0, True: 0}
+    length, at = 1100, 1 << 36                                 # more than one workgroup along the sequence
+    for k in range(300):
+        batch, dim = rng.choice([1, 2, 3]), rng.choice([1, 2, 5])
+        ld = dim + rng.choice([0, 1, dim, dim + 3])
+        stride = ld * (length - 1) + dim + rng.choice([0, ld - dim, 3, 2 * ld])
+        if k % 2:                                              # sequence-major
+            stride = dim + rng.choice([0, 1, dim, dim + 3])
+            ld = stride * (batch - 1) + dim + rng.choice([0, stride - dim, 3, 2 * stride])
+        d = abs(rng.choice([0, 1, 2]) * stride + rng.choice([0, 1, 2, length]) * ld + rng.randint(-dim - 2, 2 * dim + 3))
+        if d == 0:
+            continue
+        same = shared(length, dim, batch, ld, stride, d)
+        seen[same] += 1
+        got = forward(batch=batch, length=length, dim=dim, a=(1 << 40, ld, stride), b=(at, ld, stride),
+                      h=(at + 2 * d, ld, stride), ws=None, wbytes=0)
+        assert got == (INVALID if same else WS), (batch, dim, ld, stride, d)
+    assert min(seen.values()) > 50
+    # halves of a joint buffer, sequence-major, and batch-major with padding that is no multiple of a row
+    for ld, stride in ((4 * 128, 128), (128, 128 * 1100 + 5)):
+        rows = dict(batch=4, length=1100, dim=64, ws=None, wbytes=0)
+        one, other = (P[0], ld, stride), (P[0] + 64 * 2, ld, stride)
+        assert forward(**rows, a=one, b=(P[1], ld, stride), h=other) == WS
+        assert forward(**rows, a=one, b=(P[1], ld, stride), h=(P[0] + 63 * 2, ld, stride)) == INVALID
+        far = {k: (P[i], ld, stride) for i, k in enumerate(("a", "h", "adj"), 8)}
+        assert adjoint(**rows, **far, da=one, db=other) == WS
+        assert adjoint(**rows, **far, da=one, db=(P[0] + 65 * 2 - 4, ld, stride)) == INVALID
+        assert adjoint(**rows, **dict(far, h=one), da=(P[1], ld, stride), db=other) == WS
+
+
 def test_an_empty_sequence_has_the_limits_of_one_step():
     """It copies the states, with as many threads."""
     none = (None, 0, 0)
