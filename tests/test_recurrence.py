@@ -268,3 +268,28 @@ def test_joint_buffers_in_either_order(dtype, length):
             assert torch.equal(p, q)
         for t in (x, y):
             assert (t[..., 0] == 7).all() and (t[..., 1 + 2 * dim:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_exponentials_of_every_gate(dtype):
+    """One step from a state of one gives the gate in fp32, both ways.  The hardware's 2^y is within a step of fp32
+    (2 u), the second part's addition half a step (u), and what the series leaves out (1.5 u) and the roundings of
+    that part are within another 2 u."""
+    import differentiable_cholesky_amd as dc
+    if dtype is torch.float32:
+        x = torch.logspace(-8, 2.5, 1 << 15, dtype=torch.float64).float()
+        a = torch.cat([x, -x])
+    else:
+        a = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(dtype)
+    a = a.cuda().view(1, 1, -1)
+    one = torch.ones(1, a.shape[-1], device="cuda")
+    zero = torch.zeros_like(a)
+    _, up = dc.chol_recurrence(a, zero, h0=one, gate="log")
+    _, _, back = dc.chol_recurrence_adjoint(a, zero, zero, h0=one, adjHlast=one, gate="log")
+    x = a.double().view(1, -1)
+    want = x.exp()
+    for got in (up, back):
+        assert torch.isnan(got[torch.isnan(x)]).all()
+        assert (got[x < -105] == 0).all() and torch.isinf(got[x > 90]).all()
+        usual = (x > -87) & (x < 88.5)
+        assert ((got.double() - want).abs() <= 5 * tu.U * want)[usual].all()
