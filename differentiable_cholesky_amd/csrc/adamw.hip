@@ -155,7 +155,8 @@ __device__ __forceinline__ void roots(const float (&x)[V], float (&root)[V])
         for (int i = 0; i < V; ++i) {
             const bool low = x[i] < 0x1p-60f, high = x[i] > 0x1p+60f;
             const float r = root_of(x[i] * (low ? 0x1p+100f : high ? 0x1p-100f : 1.f));
-            root[i] = x[i] > 0.f && x[i] < INFINITY ? r * (low ? 0x1p-50f : high ? 0x1p+50f : 1.f) : x[i];
+            const float other = x[i] < 0.f ? NAN : x[i]; // zero, inf and NaN are their own roots
+            root[i] = x[i] > 0.f && x[i] < INFINITY ? r * (low ? 0x1p-50f : high ? 0x1p+50f : 1.f) : other;
         }
     }
 }

@@ -299,3 +299,20 @@ def test_a_non_finite_gradient_stays_in_its_element(bad, bits):
     if bits == 8:
         for k in ("m_scale", "v_scale"):
             assert torch.equal(runs[0][k][0], runs[1][k][0]), k
+
+
+def test_a_negative_second_moment_has_no_root():
+    """A state that no step writes: its weight is NaN, not silently stepped; zeros of either sign are zero."""
+    import differentiable_cholesky_amd as dc
+    n = 600
+    before = make(torch.float32, False, 32, seed=14, sizes=[n])
+    before["g"][0].zero_()
+    v = before["v"][0]
+    bad = torch.zeros(n, dtype=torch.bool)
+    bad[[0, 5, 300, 599]] = True
+    v[bad] = -torch.tensor([1e-6, 1.0, 1e-30, float("inf")])
+    v[[7, 8]] = torch.tensor([0.0, -0.0])
+    t, _ = on_gpu(before)
+    dc.chol_adamw(dc.chol_adamw_list(t["p"], t["g"], t["m"], t["v"]), **dict(HYPER, eps=1e-3))
+    p = t["p"][0].cpu()
+    assert torch.isnan(p[bad]).all() and torch.isfinite(p[~bad]).all()

@@ -45,3 +45,23 @@ def test_a_state_replaced_in_place(length, batch, dim, dtype, gate):
         da, db, _ = dc.chol_recurrence_adjoint(a, h, adj, h0=h0, adjHlast=d, adjH0=d, gate=gate)
         for x, y in zip((da, db, d), grads):
             assert torch.equal(x, y), k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("length", [1, 1500])
+def test_a_kept_state_captured_into_a_graph(length):
+    """Each replay carries the state on, one step or a longer piece at a time, as eager calls do."""
+    import differentiable_cholesky_amd as dc
+    a, b, _, h0, _ = make(4, length, 300, torch.bfloat16, "log", 21)
+    s, t = h0.clone(), h0.clone()
+    dc.chol_recurrence(a, b, h0=h0, gate="log")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h, _ = dc.chol_recurrence(a, b, h0=s, hlast=s, gate="log")
+    for k in range(5):
+        graph.replay()
+        want, _ = dc.chol_recurrence(a, b, h0=t, hlast=t, gate="log")
+        torch.cuda.synchronize()
+        assert torch.equal(h, want) and torch.equal(s, t), k
+        b.mul_(-0.5)
