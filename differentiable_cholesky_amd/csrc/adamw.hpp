@@ -8,9 +8,10 @@
 namespace chol {
 
 constexpr int ADAMW_TILE = 256;            // elements that share a scale of an 8-bit state
-constexpr int ADAMW_CHUNK = 4096;          // elements of a workgroup
+constexpr int ADAMW_CHUNK = 4096;          // elements of a table entry, 16 workgroups of a tile each
 
-// A workgroup's part of one tensor; the device table is an array of these.
+// A piece of one tensor, stepped by ADAMW_CHUNK / ADAMW_TILE workgroups of one wave; the
+// device table is an array of these.
 struct AdamwChunk {
     void *p;
     const void *g;

@@ -19,8 +19,8 @@
 //
 // Every element is read once and written once and costs a few operations, so
 // memory bounds long sequences: 1 x 65536 x 2048 bf16 forward 151 us (5.3 TB/s),
-// adjoint 258 us (5.2 TB/s), where a large copy reaches 5.2 TB/s; 8 x 4096 x 2048
-// 89 us (4.5 TB/s), four rounds of workgroups, whose first loads and last stores
+// adjoint 260 us (5.2 TB/s), where a large copy reaches 5.2 TB/s; 8 x 4096 x 2048
+// 91 us (4.4 TB/s), four rounds of workgroups, whose first loads and last stores
 // overlap nothing.
 #include <algorithm>
 #include <type_traits>

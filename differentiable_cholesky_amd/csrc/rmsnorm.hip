@@ -403,7 +403,9 @@ template <typename T, typename F> chol_status with_shape(int64_t n, F f)
     if (n <= 512) return f(integral_constant<int, 256>(), integral_constant<int, 2>());
     if (n <= 1024) return f(integral_constant<int, 512>(), integral_constant<int, 2>());
     if (n <= 2048) return f(integral_constant<int, 1024>(), integral_constant<int, 2>());
-    if constexpr (sizeof(T) == 4) // 16-bit rows of the longest kind end above
+    // 16-bit rows of the longest kind end above.  (The adjoint spills 32 of its registers
+    // here: 1024 threads leave 128 each, and h, adj, adj_h, w and the sums take 80.)
+    if constexpr (sizeof(T) == 4)
         if (n <= 4096) return f(integral_constant<int, 1024>(), integral_constant<int, 4>());
     return CHOL_ERR_NOT_SUPPORTED;
 }

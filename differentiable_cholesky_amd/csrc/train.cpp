@@ -1,4 +1,4 @@
-// C-ABI of the operators a training or decoding step runs next to the factor:
+// C-ABI of the operators of a recurrent model's training and decoding steps:
 // the gated linear recurrence, the RMS norm and the AdamW step.  Every check
 // runs on the host before anything is launched; a failed check launches
 // nothing.

@@ -441,7 +441,7 @@ chol_status chol_potrs_adjoint_batched(chol_dtype dtype, int64_t n, int64_t nrhs
  *   h0     [in]  device fp32 [batch, dim], the state before the first step;
  *          NULL is zero.
  *   hlast  [out] device fp32 [batch, dim], the state after the last step.
- *          hlast == h0 updates a kept state in place (decoding: len = 1).
+ *          hlast == h0 updates a kept state in place, for any len.
  *          len = 0 copies h0.
  *   h      [out] device, laid out like a and b.  h may be a or b itself (same
  *          ld and stride); otherwise it shares no element with them.  Column
@@ -497,7 +497,10 @@ chol_status chol_recurrence_workspace_size(chol_dtype dtype, int64_t batch, int6
  * chol_rmsnorm -- RMS norm of the rows of x, with the residual's addition:
  *     h = x + residual (rounded to dtype; h = x without a residual),
  *     y = h w / sqrt(mean(h^2) + eps).
- *   dtype     CHOL_F32, CHOL_BF16 or CHOL_F16, of every array; sums in fp32.
+ *   dtype     CHOL_F32, CHOL_BF16 or CHOL_F16, of every array; sums in fp32,
+ *             whose range the squares of a row are meant to stay in: where
+ *             their sum overflows (|h| near 1e19), y is zero, and where all of
+ *             them underflow (|h| below 1e-19), only eps is left.
  *   rows, cols  cols <= CHOL_RMSNORM_MAX_COLS (more returns
  *             CHOL_ERR_NOT_SUPPORTED); rows == 0 or cols == 0 is a no-op.
  *   x         [in]  device, rows of leading dimension ldx (>= cols).
