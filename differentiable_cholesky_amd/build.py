@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libchol.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["small.hip", "blocked.hip", "api.cpp", "profile.cpp", "side.cpp", "plan.cpp", "stream.hip", "solve.hip", "upper.hip", "complex.hip",
-           "recurrence.hip", "rmsnorm.hip", "adamw.hip", "train.cpp"]
+           "recurrence.hip", "rmsnorm.hip", "adamw.hip", "train.cpp",
+           "conv.hip", "scan.hip", "logprob.hip", "language.cpp"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -1,0 +1,452 @@
+// Log probabilities of given tokens, entropy and the most likely alternatives of rows of
+// logits, and the gradient that reaches the logits.
+//
+//   y = scale x,  m = max y,  s = sum e^(y - m),  lse = m + log s,  logp = y_token - lse
+//   entropy = log s - sum (y - m) e^(y - m) / s
+//   adj_x_j = scale (gl (1[j = token] - p_j) - ge p_j (log p_j + entropy)),  p = e^(y - lse)
+//
+// Memory bounds both: forward reads a row once, the adjoint reads and writes it once.  A
+// row is cut into chunks that stay in the registers of a wave (short rows, four to a
+// workgroup) or of a workgroup, so that the maximum, the sums relative to it and the
+// search for alternatives take one reading.  Several chunks a row (long rows, or few of
+// them) are joined by a second launch, one wave a row.
+//
+// Alternatives: a wave's k-th largest maximum of a lane is a bound that k elements reach,
+// so elements below it are out; those that remain, hardly more than k, are ranked one
+// after the other.  Where more remain than a wave holds (equal values, sorted rows) the
+// wave finds each in turn among its registers, k times the comparisons.  Order: by value,
+// then by the lower index; NaN before all.
+#include <algorithm>
+#include <climits>
+#include <type_traits>
+
+#include "../../include/libchol.h"
+#include "logprob.hpp"
+#include "rows.hpp"
+
+namespace chol {
+
+namespace {
+
+constexpr int WAVE = 64, THREADS = 256, WAVES = THREADS / WAVE;
+constexpr int MOST_CHUNKS = WAVE; // a lane each when they are joined
+constexpr int NONE = INT_MIN;     // below the key of any value
+
+template <typename T> constexpr int vec_of = 16 / (int)sizeof(T);
+
+// Integers in the order of the values.
+__device__ __forceinline__ int key_of(float x)
+{
+    const int b = x != x ? 0x7fc00000 : __float_as_int(x + 0.f); // (-0 is 0)
+    return b ^ (b >> 31 & 0x7fffffff);
+}
+__device__ __forceinline__ float value_of(int key) { return __int_as_float(key ^ (key >> 31 & 0x7fffffff)); }
+
+__device__ __forceinline__ float wave_max(float x)
+{
+#pragma unroll
+    for (int o = WAVE / 2; o > 0; o /= 2)
+        x = fmaxf(x, __shfl_xor(x, o));
+    return x;
+}
+__device__ __forceinline__ float wave_sum(float x)
+{
+#pragma unroll
+    for (int o = WAVE / 2; o > 0; o /= 2)
+        x += __shfl_xor(x, o);
+    return x;
+}
+__device__ __forceinline__ int wave_max(int x)
+{
+#pragma unroll
+    for (int o = WAVE / 2; o > 0; o /= 2)
+        x = max(x, __shfl_xor(x, o));
+    return x;
+}
+__device__ __forceinline__ int wave_min(int x)
+{
+#pragma unroll
+    for (int o = WAVE / 2; o > 0; o /= 2)
+        x = min(x, __shfl_xor(x, o));
+    return x;
+}
+
+struct Entry {
+    int key, index;
+};
+
+// The first of the lanes' entries, in every lane; NONE if there is none.
+__device__ __forceinline__ Entry wave_first(Entry e)
+{
+    const int key = wave_max(e.key);
+    return {key, wave_min(e.key == key ? e.index : INT_MAX)};
+}
+
+// A row's statistics, or a chunk's: its maximum, sum e and sum (x - m) e, with e =
+// 2^((x - m) k).  Without a value above -inf: -inf, 0, 0.
+struct Stats {
+    float m, s, t;
+};
+
+__device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stats st, const void *x, float given)
+{
+    const float log_s = __builtin_amdgcn_logf(st.s) * LN2;
+    const float lse = st.m == -INFINITY ? -INFINITY : fmaf(a.scale, st.m, log_s);
+    a.lse[row] = st.s != st.s ? st.s : lse; // NaN
+    const int64_t token = a.tokens[row];
+    a.logp[row] = token < 0 || token >= a.vocab  ? 0.f
+                  : given == -INFINITY && st.s == st.s ? -INFINITY
+                                                 : fmaf(a.scale, given, -a.lse[row]);
+    if (a.entropy)
+        a.entropy[row] = st.m == -INFINITY && st.s == st.s ? 0.f : log_s - a.scale * (st.t / st.s);
+}
+
+template <typename T> __device__ __forceinline__ float given_logit(const LogprobArgs &a, int64_t row)
+{
+    const int64_t token = a.tokens[row];
+    return token < 0 || token >= a.vocab ? 0.f : (float)((const T *)a.x)[row * a.ld + token];
+}
+
+// Chunk of TEAM waves with NV vectors a lane; part: a row of `chunks` statistics and
+// lists a row of logits, or nothing where the chunk is the row.
+template <typename T, int NV, int TEAM, bool TOP>
+__global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, int chunk, Stats *stats, Entry *lists)
+{
+    constexpr int V = vec_of<T>, LANES = TEAM * WAVE, N = NV * V, MOST = CHOL_LOGPROB_MAX_TOP;
+    __shared__ Stats s_stats[WAVES];
+    __shared__ Entry s_some[TOP ? WAVES : 1][WAVE], s_list[TOP ? WAVES : 1][MOST];
+    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE, t = threadIdx.x % LANES;
+    const int64_t unit = (int64_t)blockIdx.x * (WAVES / TEAM) + (TEAM == 1 ? wave : 0);
+    if (unit >= a.rows * chunks) // (waves of their own where TEAM is 1)
+        return;
+    const int64_t row = unit / chunks;
+    const int c0 = (int)(unit % chunks) * chunk, end = (int)(c0 + chunk < a.vocab ? c0 + chunk : a.vocab);
+    const T *p = (const T *)a.x + row * a.ld;
+    vec<T, V> x[NV];
+    if (c0 + LANES * N <= end) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            x[i] = load_vec<T, V>(p + c0 + (i * LANES + t) * V);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + (i * LANES + t) * V;
+            x[i] = load_some<T, V>(p + c, end - c, (T)-INFINITY);
+        }
+    }
+    const float k2 = a.scale * LOG2E;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            m = fmaxf(m, (float)x[i][v]);
+    m = wave_max(m);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float s = 0.f, w = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float d = (float)x[i][v] - ref, e = __builtin_amdgcn_exp2f(d * k2);
+            s += e;
+            w = fmaf(fmaxf(d, -1e30f), e, w); // (e is 0 at -inf)
+        }
+    s = wave_sum(s), w = wave_sum(w);
+    const Stats mine{m, s, w};
+
+    if constexpr (TOP) {
+        const int top = a.top;
+        const auto key_at = [&](int i, int v) {
+            const int c = c0 + (i * LANES + t) * V + v;
+            return c < end ? key_of((float)x[i][v]) : NONE;
+        };
+        // the bound
+        int best = NONE;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                best = max(best, key_at(i, v));
+        int bound = NONE;
+        for (int r = 0; r < top; ++r) {
+            bound = wave_max(best);
+            const uint64_t who = __ballot(best == bound);
+            if (lane == __ffsll((unsigned long long)who) - 1)
+                best = NONE;
+        }
+        bound = max(bound, NONE + 1);
+        int count = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int key = key_at(i, v);
+                const uint64_t who = __ballot(key >= bound);
+                if (who) {
+                    const int at = count + __builtin_amdgcn_mbcnt_hi((unsigned)(who >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)who, 0));
+                    if (key >= bound && at < WAVE)
+                        s_some[wave][at] = {key, c0 + (i * LANES + t) * V + v};
+                    count += __popcll(who);
+                }
+            }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if (count <= WAVE) {
+            Entry e{NONE, INT_MAX};
+            if (lane < count)
+                e = s_some[wave][lane];
+            for (int r = 0; r < top; ++r) {
+                const Entry f = wave_first(e);
+                if (e.key == f.key && e.index == f.index)
+                    e.key = NONE;
+                if (lane == 0)
+                    s_list[wave][r] = f;
+            }
+        } else {
+            Entry last{INT_MAX, -1};
+            for (int r = 0; r < top; ++r) {
+                Entry e{NONE, INT_MAX};
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) { // (columns rise, so the first of equal ones stays)
+                        const int key = key_at(i, v), c = c0 + (i * LANES + t) * V + v;
+                        const bool after = key < last.key || (key == last.key && c > last.index);
+                        if (after && key > e.key)
+                            e = {key, c};
+                    }
+                last = wave_first(e);
+                if (lane == 0)
+                    s_list[wave][r] = last;
+            }
+        }
+    }
+
+    Stats all = mine;
+    if constexpr (TEAM > 1) {
+        if (lane == 0)
+            s_stats[wave] = mine;
+        __syncthreads();
+        if (wave > 0)
+            return;
+#pragma unroll
+        for (int i = 0; i < TEAM; ++i)
+            all.m = fmaxf(all.m, s_stats[i].m);
+        all.s = all.t = 0.f;
+#pragma unroll
+        for (int i = 0; i < TEAM; ++i) {
+            const Stats o = s_stats[i];
+            if (o.m > -INFINITY || o.s != o.s) {
+                const float d = o.m - all.m, e = __builtin_amdgcn_exp2f(d * k2);
+                all.s = fmaf(o.s, e, all.s);
+                all.t = fmaf(fmaf(d, o.s, o.t), e, all.t);
+            }
+        }
+    } else {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+    if (lane == 0) {
+        if (chunks > 1)
+            stats[unit] = all;
+        else
+            finish(a, row, all, a.x, given_logit<T>(a, row));
+    }
+    if constexpr (TOP) {
+        const float lse = all.m == -INFINITY ? -INFINITY : fmaf(a.scale, all.m, __builtin_amdgcn_logf(all.s) * LN2);
+        // the waves' lists, a lane its place in one of them; TEAM * top entries
+        int at = 0;
+        for (int r = 0; r < a.top; ++r) {
+            Entry f;
+            if constexpr (TEAM == 1) {
+                f = s_list[wave][r];
+            } else {
+                Entry e{NONE, INT_MAX};
+                if (lane < TEAM && at < a.top)
+                    e = s_list[lane][at];
+                f = wave_first(e);
+                if (lane < TEAM && e.key == f.key && e.index == f.index)
+                    ++at;
+            }
+            if (lane == 0) {
+                if (chunks > 1) {
+                    lists[unit * a.top + r] = f;
+                } else {
+                    const float x = value_of(f.key);
+                    a.top_ids[row * a.top + r] = f.index;
+                    a.top_logp[row * a.top + r] = x == -INFINITY && all.s == all.s ? x : fmaf(a.scale, x, -lse);
+                }
+            }
+        }
+    }
+}
+
+// Joins a row's chunks, a lane each.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) k_logprob_join(LogprobArgs a, int chunks, const Stats *stats, const Entry *lists)
+{
+    const int lane = threadIdx.x % WAVE;
+    const int64_t row = (int64_t)blockIdx.x * WAVES + threadIdx.x / WAVE;
+    if (row >= a.rows)
+        return;
+    const float k2 = a.scale * LOG2E, given = given_logit<T>(a, row);
+    Stats st{-INFINITY, 0.f, 0.f};
+    if (lane < chunks)
+        st = stats[row * chunks + lane];
+    Stats all;
+    all.m = wave_max(st.m);
+    float s = 0.f, t = 0.f;
+    if (st.m > -INFINITY || st.s != st.s) {
+        const float d = st.m - all.m, e = __builtin_amdgcn_exp2f(d * k2);
+        s = st.s * e;
+        t = fmaf(d, st.s, st.t) * e;
+    }
+    all.s = wave_sum(s), all.t = wave_sum(t);
+    if (lane == 0)
+        finish(a, row, all, a.x, given);
+    const float lse = all.m == -INFINITY ? -INFINITY : fmaf(a.scale, all.m, __builtin_amdgcn_logf(all.s) * LN2);
+    const Entry *list = lists + (row * chunks + lane) * a.top;
+    int at = 0;
+    Entry e{NONE, INT_MAX};
+    if (lane < chunks && a.top > 0)
+        e = list[0];
+    for (int r = 0; r < a.top; ++r) {
+        const Entry f = wave_first(e);
+        if (e.key == f.key && e.index == f.index) {
+            ++at;
+            e = at < a.top ? list[at] : Entry{NONE, INT_MAX};
+        }
+        if (lane == 0) {
+            const float x = value_of(f.key);
+            a.top_ids[row * a.top + r] = f.index;
+            a.top_logp[row * a.top + r] = x == -INFINITY && all.s == all.s ? x : fmaf(a.scale, x, -lse);
+        }
+    }
+}
+
+// A thread NV vectors of one row.
+template <typename T, int NV>
+__global__ void __launch_bounds__(THREADS) k_logprob_adjoint(LogprobAdjArgs a, int64_t across)
+{
+    constexpr int V = vec_of<T>;
+    const int64_t row = blockIdx.x / across;
+    const int c0 = (int)(blockIdx.x % across) * (THREADS * NV * V);
+    const int64_t token = a.tokens[row];
+    const float lse = a.lse[row], H = a.adj_entropy ? a.entropy[row] : 0.f, ge = a.adj_entropy ? a.adj_entropy[row] : 0.f;
+    const float gl = a.adj_logp && token >= 0 && token < a.vocab ? a.adj_logp[row] : 0.f;
+    const T *x = (const T *)a.x + row * a.ld;
+    T *d = (T *)a.adj + row * a.lda;
+    vec<T, V> in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = c0 + (i * THREADS + threadIdx.x) * V;
+        in[i] = load_some<T, V>(x + c, a.vocab - c);
+    }
+    const bool empty = lse == -INFINITY; // no token is possible: zeros
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = c0 + (i * THREADS + threadIdx.x) * V;
+        vec<T, V> out;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float lp = fmaf(a.scale, (float)in[i][v], -lse), p = __builtin_amdgcn_exp2f(lp * LOG2E);
+            float g = -p * fmaf(ge, fmaxf(lp, -1e30f) + H, gl); // (p is 0 at -inf)
+            if (c + v == token)
+                g += gl;
+            out[v] = (T)(empty ? 0.f : a.scale * g);
+        }
+        store_some<T, V>(d + c, a.vocab - c, out);
+    }
+}
+
+struct Plan {
+    int team;     // waves
+    int vectors;  // of a lane
+    int chunks, chunk;
+};
+
+Plan plan_of(chol_dtype dt, int64_t rows, int64_t vocab)
+{
+    const int v = 16 / (int)lowp_size(dt);
+    Plan p;
+    p.team = vocab <= WAVE * 8 * v ? 1 : WAVES;
+    const int64_t lanes = p.team * WAVE;
+    // Eight vectors a lane, or two where the rows are short or would leave CUs without
+    // work (fewer than two workgroups for each).
+    const int64_t wide = lanes * 8 * v, narrow = lanes * 2 * v;
+    const bool small = vocab <= narrow ||
+                       (p.team > 1 && rows * ((vocab + wide - 1) / wide) < 512 && vocab <= narrow * MOST_CHUNKS);
+    p.vectors = small ? 2 : 8;
+    const int64_t most = small ? narrow : wide;
+    p.chunks = (int)std::max<int64_t>(1, (vocab + most - 1) / most);
+    // chunks of one size, a multiple of a vector
+    p.chunk = (int)(((vocab + p.chunks - 1) / p.chunks + v - 1) / v * v);
+    return p;
+}
+
+int64_t ceil_of(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int ADJ_VECTORS = 4;
+
+} // namespace
+
+size_t logprob_workspace(chol_dtype dt, int64_t rows, int64_t vocab, int top)
+{
+    const Plan p = plan_of(dt, rows, vocab);
+    return p.chunks > 1 ? (size_t)(rows * p.chunks) * (sizeof(Stats) + top * sizeof(Entry)) : 0;
+}
+
+bool logprob_fits(chol_dtype dt, int64_t rows, int64_t vocab)
+{
+    const Plan p = plan_of(dt, rows, vocab);
+    const int64_t v = 16 / (int64_t)lowp_size(dt);
+    return (double)rows * std::max<int64_t>(p.chunks, ceil_of(vocab, THREADS * ADJ_VECTORS * v)) * THREADS <= 4294967295.0;
+}
+
+chol_status logprob(chol_dtype dt, const LogprobArgs &a, void *ws, hipStream_t st)
+{
+    const Plan p = plan_of(dt, a.rows, a.vocab);
+    Stats *stats = (Stats *)ws;
+    Entry *lists = (Entry *)(stats + a.rows * p.chunks);
+    return with_lowp(dt, [&](auto *e) {
+        typedef std::remove_pointer_t<decltype(e)> T;
+        const dim3 grid((unsigned)ceil_of(a.rows * p.chunks, WAVES / p.team));
+        const auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, st, a, p.chunks, p.chunk, stats, lists);
+        };
+        const auto with_top = [&](auto nv, auto team) {
+            a.top > 0 ? launch(k_logprob<T, nv, team, true>) : launch(k_logprob<T, nv, team, false>);
+        };
+        typedef std::integral_constant<int, 1> One;
+        typedef std::integral_constant<int, 2> Two;
+        typedef std::integral_constant<int, WAVES> All;
+        typedef std::integral_constant<int, 8> Eight;
+        if (p.team == 1)
+            p.vectors == 2 ? with_top(Two(), One()) : with_top(Eight(), One());
+        else
+            p.vectors == 2 ? with_top(Two(), All()) : with_top(Eight(), All());
+        CHOL_LAUNCH_CHECK();
+        if (p.chunks > 1) {
+            hipLaunchKernelGGL(k_logprob_join<T>, dim3((unsigned)ceil_of(a.rows, WAVES)), dim3(THREADS), 0, st, a, p.chunks,
+                               (const Stats *)stats, (const Entry *)lists);
+            CHOL_LAUNCH_CHECK();
+        }
+        return CHOL_OK;
+    });
+}
+
+chol_status logprob_adjoint(chol_dtype dt, const LogprobAdjArgs &a, hipStream_t st)
+{
+    return with_lowp(dt, [&](auto *e) {
+        typedef std::remove_pointer_t<decltype(e)> T;
+        const int64_t across = ceil_of(a.vocab, THREADS * ADJ_VECTORS * vec_of<T>);
+        hipLaunchKernelGGL((k_logprob_adjoint<T, ADJ_VECTORS>), dim3((unsigned)(a.rows * across)), dim3(THREADS), 0, st, a, across);
+        CHOL_LAUNCH_CHECK();
+        return CHOL_OK;
+    });
+}
+
+} // namespace chol

@@ -1,0 +1,958 @@
+// The selective state space scan and its adjoint.
+//
+//   dt_t = softplus(delta_t + bias) (or delta_t + bias),
+//   h_t = exp(dt_t A) h_{t-1} + dt_t u_t B_t          (N states a channel)
+//   y_t = (sum_n C_t h_t + D u_t) silu(z_t)           (without z: the sum)
+//
+// and with a_t the gradient of the sum, from the last step,
+//
+//   g_t = C_t a_t + mu_{t+1},  mu_t = exp(dt_t A) g_t
+//   adj_C = sum_c a h,  adj_B = sum_c g dt u          (over the channels of the group)
+//   s_t = sum_n g B,  adj_u = dt s + D a,  adj_dt = u s + sum_n A mu h_{t-1}
+//   adj_A = sum dt mu h_{t-1},  adj_D = sum a u,  adj_h0 = mu_0
+//
+// An exponential and four more operations a state and step forward: 8 + 16 cycles of a
+// SIMD a wave, more than the channel's four 16-bit numbers cost in memory for 16 states.
+// So the vector units bound it, and the layout serves them.  A wave holds 16 channels:
+// lane l has channel l % 16 and R consecutive states, those of row l / 16 of the wave
+// (16 lanes).  Then B and C are the same along a row: one register holds them for 16 / R
+// steps and an operand of the multiplication broadcasts a lane of it (DPP).  Sums over
+// the states are within the lane and over four rows; four steps' sums at once take
+// three swaps of rows and leave each lane the sum of one step and channel, which is also
+// how u, delta and z are loaded and y is stored: nothing of a step and channel is
+// computed twice.  Only dt and dt u go from the lane that has them to the others, in LDS
+// of the wave's own.
+//
+// Where batch and channels give too few waves, sequences are cut into segments.  A first
+// launch walks each from a state of zero to its end, whose state, with the sum of its
+// steps, is a map x -> exp(A sum dt) x + Q; the segments' own walks compose the maps
+// before them.  No workgroup waits for another, and every sum has one order.
+//
+// The adjoint starts from states that the forward saved every `scan_block` steps, walks
+// a part of a block forward in registers (R * T states and their exponentials a lane)
+// and then back.  Sums over the channels take the lanes of a row, the waves of the
+// workgroup, and by a second launch the workgroups.
+#include <algorithm>
+#include <type_traits>
+#include <utility>
+
+#include "scan.hpp"
+
+namespace chol {
+
+namespace {
+
+constexpr int WAVE = 64, ROW = 16; // lanes; channels of a wave
+
+template <int I> using index = std::integral_constant<int, I>;
+template <typename F, int... I> __device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>)
+{
+    (f(index<I>()), ...);
+}
+template <int N, typename F> __device__ __forceinline__ void each(F f)
+{
+    each_of(f, std::make_integer_sequence<int, N>());
+}
+
+template <int CTRL> __device__ __forceinline__ float dpp(float x)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+// lane K of the lane's row
+template <int K> __device__ __forceinline__ float of_row(float x) { return dpp<0x150 + K>(x); }
+
+struct Two {
+    float a, b;
+};
+__device__ __forceinline__ Two swap_halves(float x, float y)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+    const unsigned p = r[0], q = r[1];
+    return {__uint_as_float(p), __uint_as_float(q)};
+}
+__device__ __forceinline__ Two swap_rows(float x, float y)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+    const unsigned p = r[0], q = r[1];
+    return {__uint_as_float(p), __uint_as_float(q)};
+}
+// Row r gets the sum over the four rows of x[r].
+__device__ __forceinline__ float over_rows(const float (&x)[4])
+{
+    const Two p = swap_halves(x[0], x[2]), q = swap_halves(x[1], x[3]);
+    const Two s = swap_rows(p.a + p.b, q.a + q.b);
+    return s.a + s.b;
+}
+// The sum over the rows, in every lane.
+__device__ __forceinline__ float over_rows(float x)
+{
+    const float same[4] = {x, x, x, x};
+    return over_rows(same);
+}
+// Lane j of a row gets the sum over the row's lanes of x[j].
+__device__ __forceinline__ float over_lanes(const float (&x)[16], int lane)
+{
+    const bool far = lane & 8, mid = lane & 4;
+    float a[8], b[4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) // rotated by 8 lanes
+        a[k] = (far ? x[k + 8] : x[k]) + dpp<0x128>(far ? x[k] : x[k + 8]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) // lanes l and l ^ 7, then l and l ^ 3 within fours: l ^ 4 up to the order in a four
+        b[k] = (mid ? a[k + 4] : a[k]) + dpp<0x141>(mid ? a[k] : a[k + 4]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        b[k] += dpp<0x4e>(b[k]); // lanes 2 3 0 1 of the four
+        b[k] += dpp<0xb1>(b[k]); // lanes 1 0 3 2
+    }
+    const float lo = lane & 1 ? b[1] : b[0], hi = lane & 1 ? b[3] : b[2];
+    return lane & 2 ? hi : lo;
+}
+
+// LDS written by lanes of a wave and read by others of the same wave, whose operations
+// on it are in order.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// log(1 + exp(x)): the larger of x and 0, and log(1 + w) with w = exp(-|x|).  Where
+// u = 1 + w is rounded, what it lost is added (the logarithm's slope there is 1 / u; w
+// is small where it matters).  The hardware's logarithm is within 1.2e-7 on all of (1, 2).
+__device__ __forceinline__ float softplus_of(float x)
+{
+    const float w = expf_of<true>(-fabsf(x)), u = 1.f + w;
+    return fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(u), LN2, w - (u - 1.f));
+}
+
+struct Plan {
+    int per_group;         // workgroups along a group's channels
+    int64_t across;        // workgroups across groups and channels
+    int segments;          // of a sequence
+    int64_t segment;       // steps of one
+};
+
+// A lane's place: its channel and its first state.
+template <int R> struct Place {
+    int row, j;            // of the wave; lane of the row
+    int g, c, n0;          // group, channel, first state
+    int64_t z, from, to;   // batch element, steps
+    int seg;
+    bool real;             // the channel exists (c is a real one in any case)
+    // false where the wave has no channel
+    __device__ __forceinline__ bool set(const ScanArgs &a, const Plan &p, int waves)
+    {
+        const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+        row = lane / ROW, j = lane % ROW;
+        const int64_t block = blockIdx.x, cb = block % p.across, rest = block / p.across;
+        seg = (int)(rest % p.segments);
+        z = rest / p.segments;
+        g = (int)(cb / p.per_group);
+        const int per = (int)(a.dim / a.groups), first = ((int)(cb % p.per_group) * waves + wave) * ROW;
+        real = first + j < per;
+        c = g * per + (real ? first + j : per - 1);
+        n0 = R * row;
+        from = seg * p.segment;
+        to = from + p.segment < a.len ? from + p.segment : a.len;
+        return first < per;
+    }
+};
+
+// Values of one step and channel a lane: steps t + 4 q + row, channel c; steps past `to`
+// are read again at the last one.
+template <typename T, int Q> struct Column {
+    T v[Q];
+    __device__ __forceinline__ void load(const SeqRows &r, int64_t z, int c, int row, int64_t t, int64_t to)
+    {
+        const T *p = (const T *)r.p + z * r.stride + c;
+        if (t + 4 * Q <= to) {
+            p += (t + row) * r.ld;
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                v[q] = p[4 * q * r.ld];
+        } else {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int64_t s = t + 4 * q + row;
+                v[q] = p[(s < to ? s : to - 1) * r.ld];
+            }
+        }
+    }
+};
+
+// B or C of STEPS steps: register k holds steps t + k * 16 / R on, lane j of a row the
+// step j / R and the row's state j % R of them.  Zero past the states' end.
+template <typename T, int R, int STEPS> struct Mixed {
+    static constexpr int PER = ROW / R, REGS = STEPS / PER;
+    T v[REGS];
+    __device__ __forceinline__ void load(const SeqRows &r, int64_t z, int g, int states, int row, int j, int64_t t, int64_t to)
+    {
+        const int n = R * row + j % R;
+        const T *p = (const T *)r.p + z * r.stride + (int64_t)g * states + (n < states ? n : states - 1);
+        if (t + STEPS <= to) {
+            p += (t + j / R) * r.ld;
+#pragma unroll
+            for (int k = 0; k < REGS; ++k)
+                v[k] = p[(int64_t)k * PER * r.ld];
+        } else {
+#pragma unroll
+            for (int k = 0; k < REGS; ++k) {
+                const int64_t s = t + k * PER + j / R;
+                v[k] = p[(s < to ? s : to - 1) * r.ld];
+            }
+        }
+        if (n >= states)
+#pragma unroll
+            for (int k = 0; k < REGS; ++k)
+                v[k] = (T)0.f;
+    }
+    __device__ __forceinline__ float at(int k) const { return (float)v[k]; }
+};
+
+// R states of a lane in an array [.., states]
+template <int R> __device__ __forceinline__ void load_states(const float *p, int n0, int states, float (&x)[R])
+{
+#pragma unroll
+    for (int i = 0; i < R; i += 4) {
+        const vec<float, 4> v = load_some<float, 4>(p + n0 + i, (int64_t)states - n0 - i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            x[i + k] = v[k];
+    }
+}
+template <int R> __device__ __forceinline__ void store_states(float *p, int n0, int states, const float (&x)[R])
+{
+#pragma unroll
+    for (int i = 0; i < R; i += 4) {
+        vec<float, 4> v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            v[k] = x[i + k];
+        store_some<float, 4>(p + n0 + i, (int64_t)states - n0 - i, v);
+    }
+}
+
+// A segment's map, for the walk that composes them: Q of every state, the steps' sum.
+struct Maps {
+    float *Q, *sum;
+    const ScanArgs &a;
+    __device__ __forceinline__ Maps(const ScanArgs &args, float *ws, int segments)
+        : Q(ws), sum(ws + (int64_t)segments * args.batch * args.dim * args.states), a(args)
+    {
+    }
+    __device__ __forceinline__ int64_t at(int seg, int64_t z, int c) const { return (seg * a.batch + z) * a.dim + c; }
+};
+
+template <typename T> __device__ __forceinline__ float step_of(T raw, float bias, bool softplus)
+{
+    const float x = (float)raw + bias;
+    return softplus ? softplus_of(x) : x;
+}
+
+constexpr int FWD_WAVES = 4, STEPS = 16;
+
+// ENDS: only walks to the end of a segment from zero and writes its map.
+template <typename T, int R, bool ENDS>
+__global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, float *ws, int block_steps)
+{
+    constexpr bool FULL = sizeof(T) == 4;
+    constexpr int Q = STEPS / 4, PER = ROW / R;
+    __shared__ float2 s_step[FWD_WAVES][STEPS][ROW];
+    __shared__ vec<float, 4> s_C[ENDS ? 1 : FWD_WAVES][STEPS][R];
+    Place<R> at;
+    if (!at.set(a, p, FWD_WAVES))
+        return;
+    const int wave = threadIdx.x / WAVE, row = at.row, j = at.j;
+    float A2[R], h[R];
+    load_states<R>(a.A + (int64_t)at.c * a.states, at.n0, a.states, A2);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        A2[i] *= LOG2E;
+        h[i] = 0.f;
+    }
+    const float bias = a.bias ? a.bias[at.c] : 0.f, D = a.D ? a.D[at.c] : 0.f;
+    const Maps maps(a, ws, p.segments);
+    // hlast may replace h0, so that where there are segments the first launch copies h0,
+    // in the place of the last segment's map, which nobody needs
+    if constexpr (ENDS) {
+        if (at.seg == p.segments - 1) {
+            if (a.h0)
+                load_states<R>(a.h0 + (at.z * a.dim + at.c) * a.states, at.n0, a.states, h);
+            at.to = at.from;
+        }
+    } else {
+        if (p.segments > 1)
+            load_states<R>(maps.Q + maps.at(p.segments - 1, at.z, at.c) * a.states, at.n0, a.states, h);
+        else if (a.h0)
+            load_states<R>(a.h0 + (at.z * a.dim + at.c) * a.states, at.n0, a.states, h);
+        for (int s = 0; s < at.seg; ++s) {
+            const int64_t m = maps.at(s, at.z, at.c);
+            const float sum = maps.sum[m];
+            float q[R];
+            load_states<R>(maps.Q + m * a.states, at.n0, a.states, q);
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                h[i] = fmaf(__builtin_amdgcn_exp2f(sum * A2[i]), h[i], q[i]);
+        }
+    }
+    float total = 0.f;
+    Column<T, Q> u, delta, zz, next_u, next_delta, next_z;
+    Mixed<T, R, STEPS> B, C, next_B, next_C;
+    const auto fetch = [&](int64_t t) {
+        next_u.load(a.u, at.z, at.c, row, t, at.to);
+        next_delta.load(a.delta, at.z, at.c, row, t, at.to);
+        next_B.load(a.B, at.z, at.g, a.states, row, j, t, at.to);
+        if constexpr (!ENDS) {
+            next_C.load(a.C, at.z, at.g, a.states, row, j, t, at.to);
+            if (a.z.p)
+                next_z.load(a.z, at.z, at.c, row, t, at.to);
+        }
+    };
+    if (at.from < at.to)
+        fetch(at.from);
+    for (int64_t t = at.from; t < at.to; t += STEPS) {
+        u = next_u, delta = next_delta, B = next_B;
+        if constexpr (!ENDS)
+            C = next_C, zz = next_z;
+        if (t + STEPS < at.to)
+            fetch(t + STEPS);
+        if constexpr (!ENDS)
+            if (a.starts && t % block_steps == 0 && at.real)
+                store_states<R>(a.starts + ((at.z * ((a.len + block_steps - 1) / block_steps) + t / block_steps) * a.dim + at.c) * a.states,
+                                at.n0, a.states, h);
+        wave_sync();
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            // a step past the end leaves the state as it is
+            const bool counts = t + 4 * q + row < at.to;
+            const float dt = counts ? step_of(delta.v[q], bias, a.softplus) : 0.f;
+            const float x = counts ? dt * (float)u.v[q] : 0.f;
+            s_step[wave][4 * q + row][j] = make_float2(dt, x);
+            if constexpr (ENDS)
+                total += dt;
+        }
+        if constexpr (!ENDS)
+#pragma unroll
+            for (int k = 0; k < Mixed<T, R, STEPS>::REGS; ++k)
+                ((float *)&s_C[wave][k * PER + j / R][0])[R * row + j % R] = C.at(k);
+        wave_sync();
+        float y[4];
+        each<STEPS>([&](auto tt) {
+            constexpr int step = tt;
+            const float2 v = s_step[wave][step][j];
+            vec<float, 4> c[R / 4];
+            if constexpr (!ENDS) {
+#pragma unroll
+                for (int k = 0; k < R / 4; ++k)
+                    c[k] = s_C[wave][step][row * (R / 4) + k];
+                y[step % 4] = 0.f;
+            }
+            const float b = B.at(step / PER);
+            each<R>([&](auto ii) {
+                constexpr int i = ii;
+                const float e = __builtin_amdgcn_exp2f(v.x * A2[i]);
+                h[i] = fmaf(e, h[i], v.y * of_row<step % PER * R + i>(b));
+                if constexpr (!ENDS)
+                    y[step % 4] = fmaf(c[i / 4][i % 4], h[i], y[step % 4]);
+            });
+            if constexpr (!ENDS && step % 4 == 3) {
+                constexpr int q = step / 4;
+                const int64_t mine = t + 4 * q + row;
+                float out = fmaf(D, (float)u.v[q], over_rows(y));
+                if (a.z.p) {
+                    const float gate = (float)zz.v[q];
+                    out *= gate * sigmoid_of<FULL>(gate);
+                }
+                if (mine < at.to && at.real)
+                    ((T *)a.y.p)[at.z * a.y.stride + mine * a.y.ld + at.c] = (T)out;
+            }
+        });
+    }
+    if constexpr (ENDS) {
+        total = over_rows(total);
+        if (at.real) {
+            const int64_t m = maps.at(at.seg, at.z, at.c);
+            store_states<R>(maps.Q + m * a.states, at.n0, a.states, h);
+            if (row == 0)
+                maps.sum[m] = total;
+        }
+    } else if (at.seg == p.segments - 1 && at.real) {
+        store_states<R>(a.hlast + (at.z * a.dim + at.c) * a.states, at.n0, a.states, h);
+    }
+}
+
+// ---------------------------------------------------------------- one step ----
+//
+// A token's work is its states, read and written once: four of a channel a lane, S lanes
+// a channel, so that a wave's states are contiguous.
+template <typename T, int S>
+__global__ void __launch_bounds__(256) k_scan_step(ScanArgs a)
+{
+    constexpr bool FULL = sizeof(T) == 4;
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / S;
+    if (at >= a.batch * a.dim)
+        return;
+    const int64_t z = at / a.dim;
+    const int c = (int)(at % a.dim), g = c / (int)(a.dim / a.groups), n0 = (threadIdx.x % S) * 4;
+    const int64_t left = a.states - n0;
+    const vec<float, 4> A = load_some<float, 4>(a.A + (int64_t)c * a.states + n0, left);
+    vec<float, 4> h = {0.f, 0.f, 0.f, 0.f};
+    if (a.h0)
+        h = load_some<float, 4>(a.h0 + at * a.states + n0, left);
+    const vec<T, 4> B = load_some<T, 4>((const T *)a.B.p + z * a.B.stride + (int64_t)g * a.states + n0, left);
+    const vec<T, 4> C = load_some<T, 4>((const T *)a.C.p + z * a.C.stride + (int64_t)g * a.states + n0, left);
+    const float dt = step_of(((const T *)a.delta.p)[z * a.delta.stride + c], a.bias ? a.bias[c] : 0.f, a.softplus);
+    const float u = (float)((const T *)a.u.p)[z * a.u.stride + c], x = dt * u;
+    const float gate = a.z.p ? (float)((const T *)a.z.p)[z * a.z.stride + c] : 0.f;
+    if (a.starts)
+        store_some<float, 4>(a.starts + at * a.states + n0, left, h);
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = fmaf(__builtin_amdgcn_exp2f(dt * (A[i] * LOG2E)), h[i], x * (float)B[i]);
+        y = fmaf((float)C[i], h[i], y);
+    }
+    store_some<float, 4>(a.hlast + at * a.states + n0, left, h);
+#pragma unroll
+    for (int o = 1; o < S; o *= 2)
+        y += __shfl_xor(y, o);
+    if (n0 == 0) {
+        y = fmaf(a.D ? a.D[c] : 0.f, u, y);
+        if (a.z.p)
+            y *= gate * sigmoid_of<FULL>(gate);
+        ((T *)a.y.p)[z * a.y.stride + c] = (T)y;
+    }
+}
+
+// ----------------------------------------------------------------- adjoint ----
+
+constexpr int BWD_WAVES = 8, PARTS = 4;     // of a block of saved states
+template <int R> constexpr int part_steps = WAVE / R; // T: R * T states of a lane in registers
+
+// Where a workgroup's sums over its channels go: [batch, groups * per_group, len, 2, 4 R]
+template <int R> __device__ __forceinline__ float *sums_at(float *part, const ScanArgs &a, const Plan &p, int64_t z, int64_t t)
+{
+    return part + ((z * p.across + blockIdx.x % p.across) * a.len + t) * (8 * R);
+}
+
+// ENDS: walks a segment back from mu = 0 and writes its map.
+template <typename T, int R>
+__global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan_adjoint_ends(ScanArgs a, Plan p, float *ws)
+{
+    constexpr bool FULL = sizeof(T) == 4;
+    constexpr int Q = STEPS / 4, PER = ROW / R;
+    __shared__ float2 s_step[FWD_WAVES][STEPS][ROW];
+    Place<R> at;
+    if (!at.set(a, p, FWD_WAVES))
+        return;
+    const int wave = threadIdx.x / WAVE, row = at.row, j = at.j;
+    float A2[R], mu[R];
+    load_states<R>(a.A + (int64_t)at.c * a.states, at.n0, a.states, A2);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        A2[i] *= LOG2E;
+        mu[i] = 0.f;
+    }
+    const float bias = a.bias ? a.bias[at.c] : 0.f;
+    // (the gradient of the end in the place of the first segment's map: adj_h0 may replace it)
+    if (at.seg == 0) {
+        if (a.adj_hlast)
+            load_states<R>(a.adj_hlast + (at.z * a.dim + at.c) * a.states, at.n0, a.states, mu);
+        if (at.real)
+            store_states<R>(Maps(a, ws, p.segments).Q + Maps(a, ws, p.segments).at(0, at.z, at.c) * a.states, at.n0,
+                            a.states, mu);
+        return;
+    }
+    float total = 0.f;
+    Column<T, Q> delta, zz, adj, next_delta, next_z, next_adj;
+    Mixed<T, R, STEPS> C, next_C;
+    const auto fetch = [&](int64_t t) {
+        next_delta.load(a.delta, at.z, at.c, row, t, at.to);
+        next_adj.load(a.adj, at.z, at.c, row, t, at.to);
+        next_C.load(a.C, at.z, at.g, a.states, row, j, t, at.to);
+        if (a.z.p)
+            next_z.load(a.z, at.z, at.c, row, t, at.to);
+    };
+    const int64_t last = at.from + (at.to - 1 - at.from) / STEPS * STEPS;
+    fetch(last);
+    for (int64_t t = last; t >= at.from; t -= STEPS) {
+        delta = next_delta, adj = next_adj, C = next_C, zz = next_z;
+        if (t > at.from)
+            fetch(t - STEPS);
+        wave_sync();
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const bool counts = t + 4 * q + row < at.to;
+            float dy = (float)adj.v[q];
+            if (a.z.p)
+                dy *= (float)zz.v[q] * sigmoid_of<FULL>((float)zz.v[q]);
+            const float dt = counts ? step_of(delta.v[q], bias, a.softplus) : 0.f;
+            s_step[wave][4 * q + row][j] = make_float2(dt, counts ? dy : 0.f);
+            total += dt;
+        }
+        wave_sync();
+        each<STEPS>([&](auto tt) {
+            constexpr int step = STEPS - 1 - tt;
+            const float2 v = s_step[wave][step][j];
+            const float c = C.at(step / PER);
+            each<R>([&](auto ii) {
+                constexpr int i = ii;
+                mu[i] = __builtin_amdgcn_exp2f(v.x * A2[i]) * (mu[i] + v.y * of_row<step % PER * R + i>(c));
+            });
+        });
+    }
+    total = over_rows(total);
+    if (at.real) {
+        const Maps maps(a, ws, p.segments);
+        const int64_t m = maps.at(at.seg, at.z, at.c);
+        store_states<R>(maps.Q + m * a.states, at.n0, a.states, mu);
+        if (row == 0)
+            maps.sum[m] = total;
+    }
+}
+
+template <typename T, int R>
+__global__ void __launch_bounds__(BWD_WAVES *WAVE, 2) k_scan_adjoint(ScanArgs a, Plan p, float *ws, float *sums, float *own)
+{
+    constexpr bool FULL = sizeof(T) == 4;
+    constexpr int TS = part_steps<R>, Q = TS / 4, PER = ROW / R, BLOCK = PARTS * TS, REGS = TS / PER;
+    static_assert(REGS == 4, "");
+    __shared__ vec<float, 4> s_step[BWD_WAVES][TS][ROW];
+    __shared__ vec<float, 4> s_B[BWD_WAVES][TS][R], s_C[BWD_WAVES][TS][R];
+    __shared__ float s_sum[2][BWD_WAVES][2][REGS][WAVE];
+    __shared__ vec<float, 4> s_state[BWD_WAVES][PARTS - 1][R / 4][WAVE];
+    Place<R> at;
+    const bool some = at.set(a, p, BWD_WAVES);
+    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE, row = at.row, j = at.j;
+    float A[R], A2[R], mu[R], dA[R];
+    load_states<R>(a.A + (int64_t)at.c * a.states, at.n0, a.states, A);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        A2[i] = A[i] * LOG2E;
+        mu[i] = dA[i] = 0.f;
+    }
+    const float bias = a.bias ? a.bias[at.c] : 0.f, D = a.D ? a.D[at.c] : 0.f;
+    if (p.segments == 1) {
+        if (a.adj_hlast)
+            load_states<R>(a.adj_hlast + (at.z * a.dim + at.c) * a.states, at.n0, a.states, mu);
+    } else {
+        const Maps maps(a, ws, p.segments);
+        load_states<R>(maps.Q + maps.at(0, at.z, at.c) * a.states, at.n0, a.states, mu);
+        for (int s = p.segments - 1; s > at.seg; --s) {
+            const int64_t m = maps.at(s, at.z, at.c);
+            const float sum = maps.sum[m];
+            float q[R];
+            load_states<R>(maps.Q + m * a.states, at.n0, a.states, q);
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                mu[i] = fmaf(__builtin_amdgcn_exp2f(sum * A2[i]), mu[i], q[i]);
+        }
+    }
+    // lanes without a channel add nothing to the sums over the channels
+    if (!at.real)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            mu[i] = 0.f;
+    float dD = 0.f, dbias = 0.f;
+    int turn = 0;
+    const int64_t blocks = (a.len + BLOCK - 1) / BLOCK;
+    const int64_t last = at.from + (at.to - 1 - at.from) / BLOCK * BLOCK;
+    for (int64_t b0 = last; b0 >= at.from; b0 -= BLOCK) {
+        float start[R];
+        load_states<R>(a.starts + ((at.z * blocks + b0 / BLOCK) * a.dim + at.c) * a.states, at.n0, a.states, start);
+        if (!at.real)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                start[i] = 0.f;
+        const int parts = (int)((at.to - b0 < BLOCK ? at.to - b0 : BLOCK) + TS - 1) / TS;
+        // the states that the parts start from
+        {
+            float h[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                h[i] = start[i];
+            for (int part = 0; part + 1 < parts; ++part) {
+                const int64_t t = b0 + part * TS;
+                Column<T, Q> u, delta;
+                Mixed<T, R, TS> B;
+                u.load(a.u, at.z, at.c, row, t, at.to);
+                delta.load(a.delta, at.z, at.c, row, t, at.to);
+                B.load(a.B, at.z, at.g, a.states, row, j, t, at.to);
+                wave_sync();
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    const float dt = at.real ? step_of(delta.v[q], bias, a.softplus) : 0.f;
+                    const vec<float, 4> v = {dt, at.real ? dt * (float)u.v[q] : 0.f, 0.f, 0.f};
+                    s_step[wave][4 * q + row][j] = v;
+                }
+                wave_sync();
+                each<TS>([&](auto tt) {
+                    constexpr int step = tt;
+                    const vec<float, 4> v = s_step[wave][step][j];
+                    const float bb = B.at(step / PER);
+                    each<R>([&](auto ii) {
+                        constexpr int i = ii;
+                        h[i] = fmaf(__builtin_amdgcn_exp2f(v[0] * A2[i]), h[i], v[1] * of_row<step % PER * R + i>(bb));
+                    });
+                });
+#pragma unroll
+                for (int k = 0; k < R / 4; ++k) {
+                    const vec<float, 4> v = {h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]};
+                    s_state[wave][part][k][lane] = v;
+                }
+            }
+        }
+        for (int part = parts - 1; part >= 0; --part) {
+            const int64_t t = b0 + part * TS;
+            Column<T, Q> u, delta, zz, adj;
+            Mixed<T, R, TS> B, C;
+            u.load(a.u, at.z, at.c, row, t, at.to);
+            delta.load(a.delta, at.z, at.c, row, t, at.to);
+            adj.load(a.adj, at.z, at.c, row, t, at.to);
+            if (a.z.p)
+                zz.load(a.z, at.z, at.c, row, t, at.to);
+            B.load(a.B, at.z, at.g, a.states, row, j, t, at.to);
+            C.load(a.C, at.z, at.g, a.states, row, j, t, at.to);
+            float first[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                first[i] = start[i];
+            if (part > 0)
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    first[i] = s_state[wave][part - 1][i / 4][lane][i % 4];
+            wave_sync();
+            float dt[Q], dy[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const bool counts = t + 4 * q + row < at.to && at.real;
+                dy[q] = (float)adj.v[q];
+                if (a.z.p)
+                    dy[q] *= (float)zz.v[q] * sigmoid_of<FULL>((float)zz.v[q]);
+                dy[q] = counts ? dy[q] : 0.f;
+                dt[q] = counts ? step_of(delta.v[q], bias, a.softplus) : 0.f;
+                const vec<float, 4> v = {dt[q], counts ? dt[q] * (float)u.v[q] : 0.f, dy[q], 0.f};
+                s_step[wave][4 * q + row][j] = v;
+            }
+#pragma unroll
+            for (int k = 0; k < REGS; ++k) {
+                ((float *)&s_B[wave][k * PER + j / R][0])[R * row + j % R] = B.at(k);
+                ((float *)&s_C[wave][k * PER + j / R][0])[R * row + j % R] = C.at(k);
+            }
+            wave_sync();
+            float h[TS][R];
+            each<TS>([&](auto tt) {
+                constexpr int step = tt;
+                const vec<float, 4> v = s_step[wave][step][j];
+                const float bb = B.at(step / PER);
+                each<R>([&](auto ii) {
+                    constexpr int i = ii;
+                    h[step][i] = fmaf(__builtin_amdgcn_exp2f(v[0] * A2[i]), step ? h[step ? step - 1 : 0][i] : first[i],
+                                      v[1] * of_row<step % PER * R + i>(bb));
+                });
+            });
+            // the exponentials are formed again: kept, they would take as many registers as h
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                asm volatile("" : "+v"(A2[i]));
+            float(*const out)[REGS][WAVE] = s_sum[turn][wave];
+            // a step's operands are on their way while the one after it is walked
+            struct {
+                vec<float, 4> v, b[R / 4], c[R / 4];
+            } now, next;
+            const auto fetch = [&](int step) {
+                next.v = s_step[wave][step][j];
+#pragma unroll
+                for (int k = 0; k < R / 4; ++k) {
+                    next.b[k] = s_B[wave][step][row * (R / 4) + k];
+                    next.c[k] = s_C[wave][step][row * (R / 4) + k];
+                }
+            };
+            fetch(TS - 1);
+            each<Q>([&](auto qq) {
+                constexpr int q = Q - 1 - qq;
+                float y[4] = {}, s1[4] = {}, s2[4] = {};
+                each<R / 4>([&](auto rr) { // registers of 16 sums: PER steps
+                    constexpr int reg = R / 4 - 1 - rr;
+                    float pB[16], pC[16];
+                    each<PER>([&](auto kk) {
+                        constexpr int at_k = PER - 1 - kk, k = reg * PER + at_k, step = 4 * q + k;
+                        now = next;
+                        if constexpr (step > 0)
+                            fetch(step - 1);
+                        __builtin_amdgcn_sched_barrier(0);
+                        const vec<float, 4> v = now.v;
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+                            const float bb = now.b[i / 4][i % 4], cc = now.c[i / 4][i % 4];
+                            const float g = fmaf(cc, v[2], mu[i]);
+                            y[k] = fmaf(cc, h[step][i], y[k]);
+                            pC[at_k * R + i] = v[2] * h[step][i];
+                            pB[at_k * R + i] = g * v[1];
+                            s1[k] = fmaf(g, bb, s1[k]);
+                            mu[i] = g * __builtin_amdgcn_exp2f(v[0] * A2[i]);
+                            const float w = mu[i] * (step ? h[step ? step - 1 : 0][i] : first[i]);
+                            s2[k] = fmaf(A[i], w, s2[k]);
+                            dA[i] = fmaf(v[0], w, dA[i]);
+                        }
+                    });
+                    out[0][q * (R / 4) + reg][lane] = over_lanes(pB, j);
+                    out[1][q * (R / 4) + reg][lane] = over_lanes(pC, j);
+                });
+                const float along = over_rows(s1), back = over_rows(s2), v = fmaf(D, (float)u.v[q], over_rows(y));
+                const int64_t mine = t + 4 * q + row;
+                if (mine < at.to && at.real) {
+                    const float x = (float)u.v[q];
+                    float ddelta = fmaf(x, along, back);
+                    if (a.softplus)
+                        ddelta *= sigmoid_of<true>((float)delta.v[q] + bias);
+                    dD = fmaf(dy[q], x, dD);
+                    dbias += ddelta;
+                    ((T *)a.adj_u.p)[at.z * a.adj_u.stride + mine * a.adj_u.ld + at.c] = (T)fmaf(dt[q], along, D * dy[q]);
+                    ((T *)a.adj_delta.p)[at.z * a.adj_delta.stride + mine * a.adj_delta.ld + at.c] = (T)ddelta;
+                    if (a.z.p) {
+                        const float gate = (float)zz.v[q], sg = sigmoid_of<FULL>(gate);
+                        ((T *)a.adj_z.p)[at.z * a.adj_z.stride + mine * a.adj_z.ld + at.c] =
+                            (T)((float)adj.v[q] * v * (sg * fmaf(gate, 1.f - sg, 1.f)));
+                    }
+                }
+            });
+            // (the other half is written while this one is read: a wave reaches the next
+            // barrier only after it has read)
+            __syncthreads();
+            for (int i = threadIdx.x; i < 2 * REGS * WAVE; i += BWD_WAVES * WAVE) {
+                const int which = i / (REGS * WAVE), reg = i / WAVE % REGS, l = i % WAVE;
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < BWD_WAVES; ++w)
+                    s += s_sum[turn][w][which][reg][l];
+                const int64_t step = t + reg * PER + l % ROW / R;
+                if (step < at.to)
+                    sums_at<R>(sums, a, p, at.z, step)[which * 4 * R + R * (l / ROW) + l % R] = s;
+            }
+            turn ^= 1;
+        }
+    }
+    dD = over_rows(dD), dbias = over_rows(dbias);
+    if (!some || !at.real)
+        return;
+    if (at.seg == 0 && a.adj_h0)
+        store_states<R>(a.adj_h0 + (at.z * a.dim + at.c) * a.states, at.n0, a.states, mu);
+    float *o = own + ((at.z * p.segments + at.seg) * a.dim + at.c) * (a.states + 2);
+    store_states<R>(o, at.n0, a.states, dA);
+    if (row == 0)
+        o[a.states] = dD, o[a.states + 1] = dbias;
+}
+
+// adj_B and adj_C: over a group's workgroups.  A thread a (step, group, state) of one.
+template <typename T>
+__global__ void __launch_bounds__(256) k_scan_mixed_sums(ScanArgs a, Plan p, const float *sums, int wide)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, count = a.batch * a.len * a.groups * 2 * a.states;
+    if (i >= count)
+        return;
+    const int n = (int)(i % a.states), which = (int)(i / a.states % 2);
+    const int64_t rest = i / a.states / 2, t = rest % a.len;
+    const int g = (int)(rest / a.len % a.groups);
+    const int64_t z = rest / a.len / a.groups;
+    const float *x = sums + ((z * p.across + (int64_t)g * p.per_group) * a.len + t) * (2 * wide) + which * wide + n;
+    const int64_t step = a.len * 2 * wide;
+    float s = 0.f;
+    for (int k = 0; k < p.per_group; ++k)
+        s += x[k * step];
+    const SeqRows &r = which ? a.adj_C : a.adj_B;
+    ((T *)r.p)[z * r.stride + t * r.ld + (int64_t)g * a.states + n] = (T)s;
+}
+
+// adj_A, adj_D and adj_bias: over batch and segments.
+__global__ void __launch_bounds__(1024) k_scan_own_sums(ScanArgs a, const float *own, int64_t rows)
+{
+    __shared__ float s_sum[16][WAVE];
+    const int lane = threadIdx.x % WAVE, slot = threadIdx.x / WAVE;
+    const int64_t i = (int64_t)blockIdx.x * WAVE + lane, cols = a.dim * (a.states + 2);
+    float s = 0.f;
+    if (i < cols)
+        for (int64_t r = slot; r < rows; r += 16)
+            s += own[r * cols + i];
+    s_sum[slot][lane] = s;
+    __syncthreads();
+    if (slot > 0 || i >= cols)
+        return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k)
+        s += s_sum[k][lane];
+    const int64_t c = i / (a.states + 2);
+    const int n = (int)(i % (a.states + 2));
+    float *out = n < a.states ? a.adj_A + c * a.states + n : n == a.states ? a.adj_D + (a.adj_D ? c : 0) : a.adj_bias + (a.adj_bias ? c : 0);
+    if (n >= a.states && !(n == a.states ? a.adj_D : a.adj_bias))
+        return;
+    *out = a.accumulate ? *out + s : s;
+}
+
+// An empty sequence's states and gradients: the given ones, or zero.
+__global__ void __launch_bounds__(256) k_scan_copy(const float *from, float *to, int64_t n)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n)
+        to[i] = from ? from[i] : 0.f;
+}
+
+int rows_of(int states) { return states <= 16 ? 4 : states <= 32 ? 8 : 16; } // R
+
+Plan plan_of(const ScanArgs &a, bool adjoint)
+{
+    Plan p;
+    const int waves = adjoint ? BWD_WAVES : FWD_WAVES, block = scan_block(a.states);
+    const int64_t per = a.dim / a.groups, wave_count = (per + ROW - 1) / ROW;
+    p.per_group = (int)((wave_count + waves - 1) / waves);
+    p.across = (int64_t)p.per_group * a.groups;
+    // Segments cost each step about as much again.
+    const int64_t all = a.batch * a.groups * wave_count, blocks = std::max<int64_t>(1, (a.len + block - 1) / block);
+    const int64_t want = all >= 768 ? 1 : std::min<int64_t>(blocks, std::min<int64_t>(64, 2048 / all));
+    const int64_t each = (blocks + want - 1) / want;
+    p.segment = each * block;
+    p.segments = (int)((blocks + each - 1) / each);
+    return p;
+}
+// where the adjoint's waves along the channels are put together in other workgroups
+Plan ends_plan(const ScanArgs &a, Plan p)
+{
+    const Plan f = plan_of(a, false);
+    p.per_group = f.per_group, p.across = f.across;
+    return p;
+}
+
+int64_t maps_size(const ScanArgs &a, const Plan &p)
+{
+    return p.segments > 1 ? p.segments * a.batch * a.dim * (int64_t)(a.states + 1) : 0;
+}
+int64_t sums_size(const ScanArgs &a, const Plan &p) { return a.batch * p.across * a.len * 8 * rows_of(a.states); }
+int64_t own_size(const ScanArgs &a, const Plan &p) { return a.batch * p.segments * a.dim * (int64_t)(a.states + 2); }
+
+template <typename F> chol_status with_rows(int states, F f)
+{
+    return states <= 16 ? f(index<4>()) : states <= 32 ? f(index<8>()) : f(index<16>());
+}
+
+int64_t ceil_of(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+chol_status copy(const float *from, float *to, int64_t n, hipStream_t st)
+{
+    if (n > 0 && to && from != to) {
+        hipLaunchKernelGGL(k_scan_copy, dim3((unsigned)ceil_of(n, 256)), dim3(256), 0, st, from, to, n);
+        CHOL_LAUNCH_CHECK();
+    }
+    return CHOL_OK;
+}
+
+int step_lanes(int states)
+{
+    int s = 1;
+    while (4 * s < states)
+        s *= 2;
+    return s;
+}
+
+bool grid_ok(double threads) { return threads <= 4294967295.0; }
+
+} // namespace
+
+int scan_block(int states) { return PARTS * WAVE / rows_of(states); }
+
+int64_t scan_workspace(const ScanArgs &a)
+{
+    const Plan p = plan_of(a, false);
+    if (!grid_ok((double)a.batch * p.across * p.segments * FWD_WAVES * WAVE) ||
+        !grid_ok((double)a.batch * a.dim * std::max(step_lanes(a.states), a.states) + 256))
+        return -1;
+    return a.len > 1 ? maps_size(a, p) * (int64_t)sizeof(float) : 0;
+}
+
+int64_t scan_adjoint_workspace(const ScanArgs &a)
+{
+    const Plan p = plan_of(a, true);
+    if (!grid_ok((double)a.batch * p.across * p.segments * BWD_WAVES * WAVE) ||
+        !grid_ok((double)a.batch * a.len * a.groups * 2 * a.states + 256) ||
+        !grid_ok((double)a.batch * a.dim * a.states + 256))
+        return -1;
+    return a.len > 0 ? (maps_size(a, p) + sums_size(a, p) + own_size(a, p)) * (int64_t)sizeof(float) : 0;
+}
+
+chol_status scan(chol_dtype dt, const ScanArgs &a, void *ws, hipStream_t st)
+{
+    if (a.len == 0)
+        return copy(a.h0, a.hlast, a.batch * a.dim * a.states, st);
+    return with_lowp(dt, [&](auto *e) {
+        typedef std::remove_pointer_t<decltype(e)> T;
+        if (a.len == 1) {
+            const int s = step_lanes(a.states);
+            const dim3 grid((unsigned)ceil_of(a.batch * a.dim * s, 256));
+            const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, a); };
+            s == 1   ? launch(k_scan_step<T, 1>)
+            : s == 2 ? launch(k_scan_step<T, 2>)
+            : s == 4 ? launch(k_scan_step<T, 4>)
+            : s == 8 ? launch(k_scan_step<T, 8>)
+                     : launch(k_scan_step<T, 16>);
+            CHOL_LAUNCH_CHECK();
+            return CHOL_OK;
+        }
+        return with_rows(a.states, [&](auto r) {
+            constexpr int R = r;
+            const Plan p = plan_of(a, false);
+            const dim3 grid((unsigned)(a.batch * p.across * p.segments));
+            const auto launch = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, grid, dim3(FWD_WAVES * WAVE), 0, st, a, p, (float *)ws, scan_block(a.states));
+            };
+            if (p.segments > 1) {
+                launch(k_scan<T, R, true>);
+                CHOL_LAUNCH_CHECK();
+            }
+            launch(k_scan<T, R, false>);
+            CHOL_LAUNCH_CHECK();
+            return CHOL_OK;
+        });
+    });
+}
+
+chol_status scan_adjoint(chol_dtype dt, const ScanArgs &a, void *ws, hipStream_t st)
+{
+    if (a.len == 0 || a.batch == 0) {
+        const chol_status s = copy(a.adj_hlast, a.adj_h0, a.batch * a.dim * a.states, st);
+        if (s != CHOL_OK || a.accumulate)
+            return s;
+        for (const auto &[to, n] : {std::pair{a.adj_A, a.dim * a.states}, std::pair{a.adj_D, a.dim}, std::pair{a.adj_bias, a.dim}}) {
+            const chol_status c = copy(nullptr, to, n, st);
+            if (c != CHOL_OK)
+                return c;
+        }
+        return CHOL_OK;
+    }
+    return with_lowp(dt, [&](auto *e) {
+        typedef std::remove_pointer_t<decltype(e)> T;
+        return with_rows(a.states, [&](auto r) {
+            constexpr int R = r;
+            const Plan p = plan_of(a, true);
+            float *maps = (float *)ws, *sums = maps + maps_size(a, p), *own = sums + sums_size(a, p);
+            if (p.segments > 1) {
+                const Plan f = ends_plan(a, p);
+                hipLaunchKernelGGL((k_scan_adjoint_ends<T, R>), dim3((unsigned)(a.batch * f.across * f.segments)),
+                                   dim3(FWD_WAVES * WAVE), 0, st, a, f, maps);
+                CHOL_LAUNCH_CHECK();
+            }
+            hipLaunchKernelGGL((k_scan_adjoint<T, R>), dim3((unsigned)(a.batch * p.across * p.segments)),
+                               dim3(BWD_WAVES * WAVE), 0, st, a, p, maps, sums, own);
+            CHOL_LAUNCH_CHECK();
+            hipLaunchKernelGGL((k_scan_mixed_sums<T>), dim3((unsigned)ceil_of(a.batch * a.len * a.groups * 2 * a.states, 256)),
+                               dim3(256), 0, st, a, p, (const float *)sums, 4 * R);
+            CHOL_LAUNCH_CHECK();
+            hipLaunchKernelGGL(k_scan_own_sums, dim3((unsigned)ceil_of(a.dim * (a.states + 2), WAVE)), dim3(1024), 0, st, a,
+                               (const float *)own, a.batch * p.segments);
+            CHOL_LAUNCH_CHECK();
+            return CHOL_OK;
+        });
+    });
+}
+
+} // namespace chol

@@ -81,7 +81,8 @@ extern "C" {
 /* Real types (fp32, fp64) for the factor, its adjoint and the solves; the complex types (interleaved real and
  * imaginary parts, complex64 = 2 x fp32, complex128 = 2 x fp64) only for the
  * chol_potrf_hermitian* family; the 16-bit types, and fp32, for the training
- * operators (chol_recurrence*, chol_rmsnorm*, chol_adamw*). */
+ * operators (chol_recurrence*, chol_rmsnorm*, chol_adamw*, chol_causal_conv*,
+ * chol_selective_scan*, chol_token_logprob*). */
 typedef enum {
     CHOL_F32 = 0,
     CHOL_F64 = 1,
@@ -619,6 +620,204 @@ typedef struct {
 chol_status chol_adamw_list(chol_dtype dtype, int bits, int64_t count, const chol_adamw_tensor *tensors,
                             void *table, size_t table_bytes, int64_t *chunks, size_t *bytes);
 
+/* Widths of chol_causal_conv's filters. */
+#define CHOL_CONV_MIN_WIDTH 2
+#define CHOL_CONV_MAX_WIDTH 4
+
+/*
+ * chol_causal_conv -- a short causal convolution along a sequence, one filter a
+ * channel:
+ *     p_t = bias + sum_{k < width} w_k x_{t-width+1+k},
+ *     y_t = p_t / (1 + exp(-p_t)) (silu != 0), or p_t.
+ *   dtype  CHOL_F32, CHOL_BF16 or CHOL_F16, of every array; sums are fp32 and
+ *          y rounds once.
+ *   width  2, 3 or 4 taps (others return CHOL_ERR_NOT_SUPPORTED).
+ *   x      [in]  device; element (i, t, c) at p[i * stride + t * ld + c], laid
+ *          out as chol_recurrence's arrays may be.
+ *   w      [in]  device [dim, width]; tap width - 1 meets the newest row.
+ *   bias   [in]  device [dim], or NULL.
+ *   state  [in]  device [batch, width - 1, dim], the rows before the first, or
+ *          NULL for zeros.
+ *   last   [out] device [batch, width - 1, dim], the last width - 1 rows of
+ *          state and x together (the state of a call that goes on), or NULL.
+ *          last == state updates kept rows in place, for any len.  len = 0
+ *          copies state.
+ *   y      [out] device, laid out like x; shares no element with an input.
+ * Outputs otherwise share no element with inputs or each other.
+ * batch * dim above 2^31 - 1, and sizes that need 2^32 threads or more, return
+ * CHOL_ERR_NOT_SUPPORTED.
+ */
+chol_status chol_causal_conv(chol_dtype dtype, int silu, int64_t batch, int64_t len, int64_t dim, int64_t width,
+                             const void *x, int64_t ldx, int64_t strideX,
+                             const void *w, const void *bias,
+                             const void *state, void *last,
+                             void *y, int64_t ldy, int64_t strideY, void *stream);
+
+/*
+ * chol_causal_conv_adjoint -- reverse-mode adjoint of chol_causal_conv.  With
+ * q_t = adj_t times the activation's slope at p_t,
+ *     adjX_t = sum_k w_k q_{t+width-1-k},   adjW_k (+)= sum_t q_t x_{t-width+1+k},
+ *     adjBias (+)= sum_t q_t.
+ *   x, w, bias, state  [in] as the forward call had them.
+ *   adj       [in]  gradient of y, laid out like x.
+ *   adjLast   [in]  gradient of last, [batch, width - 1, dim], or NULL for zero.
+ *   adjX      [out] like x.
+ *   adjW      [out] fp32 [dim, width]; adjBias [out] fp32 [dim], or NULL.
+ *             accumulate != 0 adds to both.  Their terms are added in an order
+ *             that depends on the sizes only.
+ *   adjState  [out] gradient of state, [batch, width - 1, dim], or NULL.
+ * Outputs share no element with inputs or each other.
+ *   workspace at least chol_causal_conv_adjoint_workspace_size bytes (4-byte
+ *             aligned; NULL allowed when it is 0).
+ */
+chol_status chol_causal_conv_adjoint(chol_dtype dtype, int silu, int64_t batch, int64_t len, int64_t dim, int64_t width,
+                                     const void *x, int64_t ldx, int64_t strideX,
+                                     const void *w, const void *bias, const void *state,
+                                     const void *adj, int64_t lda, int64_t strideA,
+                                     const void *adjLast,
+                                     void *adjX, int64_t ldax, int64_t strideAX,
+                                     float *adjW, float *adjBias, int accumulate, void *adjState,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace chol_causal_conv_adjoint needs. */
+chol_status chol_causal_conv_adjoint_workspace_size(chol_dtype dtype, int64_t batch, int64_t len, int64_t dim,
+                                                    int64_t width, size_t *bytes);
+
+/* Most states of a channel of the selective scan. */
+#define CHOL_SCAN_MAX_STATES 64
+
+/* A [batch, len, columns] array of the selective scan in device memory: element
+ * (i, t, c) at p[i * stride + t * ld + c].  The batch may lie outside the rows
+ * (stride >= ld * (len-1) + columns) or, in sequence-major storage, inside (ld >=
+ * stride * (batch-1) + columns). */
+typedef struct {
+    void *p;
+    int64_t ld, stride;
+} chol_rows;
+
+/*
+ * Arguments of chol_selective_scan and its adjoint (host memory, read during the
+ * call).  For every channel c of `dim`, and every one of its `states` numbers n,
+ *     dt_t = log(1 + exp(delta_t + bias)) (softplus != 0), or delta_t + bias,
+ *     h_t[n] = exp(dt_t A[c, n]) h_{t-1}[n] + dt_t u_t B_t[g, n],
+ *     s_t = sum_n C_t[g, n] h_t[n] + D u_t,
+ *     y_t = s_t z_t / (1 + exp(-z_t)), or s_t where z.p is NULL,
+ * where g = c / (dim / groups) is the channel's group.
+ *   u, delta, z  [in] [batch, len, dim] of dtype.
+ *   B, C     [in] [batch, len, groups * states] of dtype.
+ *   A        [in] fp32 [dim, states]; D, bias [in] fp32 [dim], or NULL for zero.
+ *   h0       [in] fp32 [batch, dim, states], the state before the first step, or
+ *            NULL for zero (the forward's; the adjoint has it in starts).
+ *   hlast    [out] fp32 [batch, dim, states], the state after the last step.
+ *            hlast == h0 updates a kept state in place, for any len.  len = 0
+ *            copies h0.
+ *   y        [out] [batch, len, dim] of dtype; may be u, delta or z itself.
+ *   starts   fp32 [batch, ceil(len / block), dim, states] with block =
+ *            chol_selective_scan_block(states): the states before every block-th
+ *            step.  The forward writes them unless it is NULL; the adjoint reads
+ *            them.
+ * The adjoint's (reverse-mode, of y and hlast):
+ *   adj      [in] gradient of y; adj_hlast [in] fp32, gradient of hlast, or NULL
+ *            for zero.
+ *   adj_u, adj_delta, adj_z  [out] of dtype, [batch, len, dim]; each may be adj
+ *            itself or its own array (adj_u u, adj_delta delta, adj_z z);
+ *            adj_delta is the gradient of delta before bias and softplus; adj_z
+ *            is not used without z.
+ *   adj_B, adj_C  [out] of dtype, laid out like B and C: sums over the channels
+ *            of a group, rounded once; may be B and C themselves.
+ *   adj_A    [out] fp32 [dim, states]; adj_D, adj_bias [out] fp32 [dim], or NULL;
+ *            accumulate != 0 adds to the three.
+ *   adj_h0   [out] fp32 [batch, dim, states], or NULL; may be adj_hlast itself.
+ * Outputs otherwise share no element with inputs or each other.
+ * States, sums and exponentials are fp32; a result does not depend on timing, and
+ * terms are added in an order that depends on the sizes only.  exp(dt A) is within
+ * (3 |dt A| + 2) 2^-24 of itself.  A long run of steps is also composed as
+ * exp(A sum dt): A of at most 0 is what that is meant for; where it overflows, the
+ * result is inf or NaN.
+ */
+typedef struct {
+    int64_t batch, len, dim, groups, states;
+    int softplus, accumulate;
+    chol_rows u, delta, B, C, z, y;
+    const float *A, *D, *bias, *h0;
+    float *hlast, *starts;
+    chol_rows adj, adj_u, adj_delta, adj_B, adj_C, adj_z;
+    const float *adj_hlast;
+    float *adj_A, *adj_D, *adj_bias, *adj_h0;
+} chol_scan_args;
+
+/*
+ * chol_selective_scan, chol_selective_scan_adjoint -- the scan of chol_scan_args,
+ * and its adjoint.  workspace: at least as many bytes as the _workspace_size
+ * call gives (4-byte aligned; NULL allowed when it is 0).
+ * states above CHOL_SCAN_MAX_STATES, batch * dim * states above 2^31 - 1, and
+ * sizes that need 2^32 threads or more, return CHOL_ERR_NOT_SUPPORTED; groups that
+ * do not divide dim return CHOL_ERR_INVALID_VALUE.
+ */
+chol_status chol_selective_scan(chol_dtype dtype, const chol_scan_args *args, void *workspace, size_t workspace_bytes,
+                                void *stream);
+chol_status chol_selective_scan_adjoint(chol_dtype dtype, const chol_scan_args *args, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that chol_selective_scan (adjoint = 0) or its adjoint needs. */
+chol_status chol_selective_scan_workspace_size(int adjoint, int64_t batch, int64_t len, int64_t dim, int64_t groups,
+                                               int64_t states, size_t *bytes);
+
+/* Steps between two of the saved states `starts`: 64, 32 or 16 for up to 16, 32 or
+ * 64 states; -1 for states outside 1 .. CHOL_SCAN_MAX_STATES. */
+int64_t chol_selective_scan_block(int64_t states);
+
+/* Most columns of chol_token_logprob, and most alternatives a row. */
+#define CHOL_LOGPROB_MAX_VOCAB 524288
+#define CHOL_LOGPROB_MAX_TOP 32
+
+/*
+ * chol_token_logprob -- log probabilities of given tokens under rows of logits x:
+ *     lse = log sum_j exp(scale x_j),   logp = scale x_token - lse,
+ *     entropy = -sum_j p_j log p_j,   p_j = exp(scale x_j - lse).
+ *   dtype   CHOL_F32, CHOL_BF16 or CHOL_F16, of the logits.
+ *   scale   positive and finite (the inverse of a temperature).
+ *   x       [in]  device [rows, vocab], leading dimension ldx.
+ *   tokens  [in]  device int64 [rows]; outside 0 .. vocab-1 a row has no token
+ *           and its logp is 0.
+ *   logp, lse  [out] device fp32 [rows]; entropy [out] device fp32 [rows], or NULL.
+ *   top     number of alternatives, 0 .. min(vocab, CHOL_LOGPROB_MAX_TOP):
+ *           top_ids [out] device int64 [rows, top], the columns of the largest
+ *           logits, the lowest first among equal ones, and top_logp [out] device
+ *           fp32 [rows, top].
+ * A logit of -inf has no probability.  A row of nothing else has lse and logp -inf
+ * and entropy 0; a row that holds NaN or +inf has NaN, as its definition has (NaN is
+ * the first of its alternatives).
+ *   workspace  at least chol_token_logprob_workspace_size bytes (8-byte aligned;
+ *           NULL allowed when it is 0).
+ * vocab above CHOL_LOGPROB_MAX_VOCAB, rows above 2^31 - 1, and sizes that need
+ * 2^32 threads or more, return CHOL_ERR_NOT_SUPPORTED; vocab = 0 with rows > 0 returns
+ * CHOL_ERR_INVALID_VALUE.
+ */
+chol_status chol_token_logprob(chol_dtype dtype, int64_t rows, int64_t vocab, const void *x, int64_t ldx,
+                               const int64_t *tokens, float scale, float *logp, float *lse, float *entropy,
+                               int64_t top, float *top_logp, int64_t *top_ids,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace chol_token_logprob needs. */
+chol_status chol_token_logprob_workspace_size(chol_dtype dtype, int64_t rows, int64_t vocab, int64_t top, size_t *bytes);
+
+/*
+ * chol_token_logprob_adjoint -- gradient of logp and entropy with respect to the
+ * logits:
+ *     adjX_j = scale (adjLogp (1[j = token] - p_j) - adjEntropy p_j (log p_j + entropy)).
+ *   x, tokens, scale  [in] as the forward call had them; lse, entropy [in] what it
+ *           wrote (entropy may be NULL where adjEntropy is).
+ *   adjLogp, adjEntropy  [in] device fp32 [rows], or NULL for zero.  A row without a
+ *           token takes no adjLogp.
+ *   adjX    [out] device [rows, vocab] of dtype, leading dimension ldax; may be x
+ *           itself.  Zero in a row whose lse is -inf.
+ */
+chol_status chol_token_logprob_adjoint(chol_dtype dtype, int64_t rows, int64_t vocab, const void *x, int64_t ldx,
+                                       const int64_t *tokens, float scale, const float *lse, const float *entropy,
+                                       const float *adjLogp, const float *adjEntropy,
+                                       void *adjX, int64_t ldax, void *stream);
+
 /*
  * chol_wave_dot_fwd_adj -- diagnostic kernel for the reduction/broadcast
  * pattern the small-tile kernels rely on (Warp issue #1374, "adj_tile_dot is
@@ -696,7 +895,13 @@ typedef enum {
     CHOL_K_RMSNORM = 16,         /* chol_rmsnorm, chol_rmsnorm_quant; bytes of the arrays read and written */
     CHOL_K_RMSNORM_ADJOINT = 17, /* chol_rmsnorm_adjoint, whole calls; bytes of the arrays read and written */
     CHOL_K_ADAMW = 18,           /* chol_adamw; bytes moved (whole chunks counted) */
-    CHOL_K_COUNT = 19
+    CHOL_K_CONV = 19,            /* chol_causal_conv; bytes: 2 * batch * len * dim * elem */
+    CHOL_K_CONV_ADJOINT = 20,    /* chol_causal_conv_adjoint, whole calls; bytes: 3 * batch * len * dim * elem */
+    CHOL_K_SCAN = 21,            /* chol_selective_scan, whole calls; bytes of u, delta, z and y */
+    CHOL_K_SCAN_ADJOINT = 22,    /* chol_selective_scan_adjoint, whole calls; bytes of u, delta, z, adj and their gradients */
+    CHOL_K_LOGPROB = 23,         /* chol_token_logprob, whole calls; bytes: rows * vocab * elem */
+    CHOL_K_LOGPROB_ADJOINT = 24, /* chol_token_logprob_adjoint; bytes: 2 * rows * vocab * elem */
+    CHOL_K_COUNT = 25
 } chol_kernel_family;
 
 #define CHOL_PROFILE_ALL 0xffffffffu
