@@ -123,7 +123,10 @@ __device__ __forceinline__ void wave_sync()
 // is small where it matters).  The hardware's logarithm is within 1.2e-7 on all of (1, 2).
 __device__ __forceinline__ float softplus_of(float x)
 {
-    const float w = expf_of<true>(-fabsf(x)), u = 1.f + w;
+    // exp(-|x|) with its product's low part (expf_of); at -110, where it is 0, and below
+    const float v = fmaxf(-fabsf(x), -110.f), y = v * LOG2E, e = __builtin_amdgcn_exp2f(y);
+    const float low = fmaf(v, (float)(1.4426950408889634074 - LOG2E), fmaf(v, LOG2E, -y));
+    const float w = fmaf(e * LN2, low, e), u = 1.f + w;
     return fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(u), LN2, w - (u - 1.f));
 }
 
@@ -131,84 +134,112 @@ struct Plan {
     int per_group;         // workgroups along a group's channels
     int64_t across;        // workgroups across groups and channels
     int segments;          // of a sequence
-    int64_t segment;       // steps of one
+    int segment;           // steps of one
+};
+
+// An array from some row on, as buffer instructions take it: the address is the wave's, the
+// offset (32 bits, unsigned) the lane's, so that a load costs no vector arithmetic.
+template <typename T> struct Buffer {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ Buffer(const char *p)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, -1, 0x00027000))
+    {
+    }
+    __device__ __forceinline__ T load(unsigned lane, unsigned wave) const
+    {
+        if constexpr (sizeof(T) == 4)
+            return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, lane, wave, 0));
+        else
+            return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, lane, wave, 0));
+    }
+    __device__ __forceinline__ void store(unsigned lane, unsigned wave, T x) const
+    {
+        if constexpr (sizeof(T) == 4)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, x), r, lane, wave, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, x), r, lane, wave, 0);
+    }
+};
+
+// N values of a lane from a block of rows, EVERY rows apart.  KEEP: an offset for each
+// value; else one, and a scalar register for each.
+template <typename T, int N, int EVERY, bool KEEP> struct Feed {
+    const char *p;     // the sequence's first row
+    unsigned ld;       // bytes
+    unsigned first, off[KEEP ? N : 1];
+    // row first + k * EVERY of a block, column col
+    __device__ __forceinline__ Feed(const SeqRows &r, int64_t z, int64_t c0, int row, int col)
+        : p((const char *)((const T *)r.p + z * r.stride + c0)), ld((unsigned)r.ld * (unsigned)sizeof(T)), first(row)
+    {
+#pragma unroll
+        for (int k = 0; k < (KEEP ? N : 1); ++k)
+            off[k] = (first + k * EVERY) * ld + col * (unsigned)sizeof(T);
+    }
+    __device__ __forceinline__ Buffer<T> block(int t) const { return Buffer<T>(p + (uint64_t)(unsigned)t * ld); }
+    __device__ __forceinline__ unsigned lane(int k) const { return off[KEEP ? k : 0]; }
+    __device__ __forceinline__ unsigned wave(int k) const { return KEEP ? 0u : k * EVERY * ld; }
+    // the block from step t; rows past `left` of them are read again at the last one
+    // (WHOLE: there are none)
+    template <bool WHOLE = false> __device__ __forceinline__ void load(T (&v)[N], int t, int left) const
+    {
+        const Buffer<T> b = block(t);
+        if (WHOLE || left >= N * EVERY) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                v[k] = b.load(lane(k), wave(k));
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const unsigned last = (unsigned)left - 1u, row = min(first + k * EVERY, last);
+                v[k] = b.load(off[0] + (row - first) * ld, 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(int t, int k, T x) const { block(t).store(lane(k), wave(k), x); }
+    __device__ __forceinline__ bool inside(int k, int left) const { return (int)first + k * EVERY < left; }
 };
 
 // A lane's place: its channel and its first state.
 template <int R> struct Place {
     int row, j;            // of the wave; lane of the row
     int g, c, n0;          // group, channel, first state
-    int64_t z, from, to;   // batch element, steps
-    int seg;
+    int64_t z;             // batch element
+    int from, to, seg;     // steps; segment
+    int first;             // the wave's first channel
     bool real;             // the channel exists (c is a real one in any case)
+    // values of one step and channel a lane: steps 4 k + row of a block, channel c
+    template <typename T, int STEPS, bool KEEP = true>
+    __device__ __forceinline__ Feed<T, STEPS / 4, 4, KEEP> column(const SeqRows &r) const
+    {
+        return {r, z, first, row, c - first};
+    }
+    // B or C: value k holds steps k * 16 / R on of a block, lane j of a row the step j / R
+    // and the row's state j % R of them
+    template <typename T, int STEPS, bool KEEP = true>
+    __device__ __forceinline__ Feed<T, STEPS * R / ROW, ROW / R, KEEP> mixed(const SeqRows &r, int states) const
+    {
+        const int n = n0 + j % R;
+        return {r, z, (int64_t)g * states, j / R, n < states ? n : states - 1};
+    }
     // false where the wave has no channel
     __device__ __forceinline__ bool set(const ScanArgs &a, const Plan &p, int waves)
     {
         const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
         row = lane / ROW, j = lane % ROW;
-        const int64_t block = blockIdx.x, cb = block % p.across, rest = block / p.across;
-        seg = (int)(rest % p.segments);
-        z = rest / p.segments;
-        g = (int)(cb / p.per_group);
-        const int per = (int)(a.dim / a.groups), first = ((int)(cb % p.per_group) * waves + wave) * ROW;
-        real = first + j < per;
-        c = g * per + (real ? first + j : per - 1);
+        const unsigned block = blockIdx.x, cb = block % (unsigned)p.across, rest = block / (unsigned)p.across;
+        seg = (int)(rest % (unsigned)p.segments);
+        z = rest / (unsigned)p.segments;
+        g = (int)(cb / (unsigned)p.per_group);
+        const int per = (int)((unsigned)a.dim / (unsigned)a.groups);
+        const int at = ((int)(cb % (unsigned)p.per_group) * waves + wave) * ROW;
+        real = at + j < per;
+        first = g * per + (at < per ? at : per - 1);
+        c = g * per + (real ? at + j : per - 1);
         n0 = R * row;
         from = seg * p.segment;
-        to = from + p.segment < a.len ? from + p.segment : a.len;
-        return first < per;
+        to = (int)min((int64_t)from + p.segment, a.len);
+        return at < per;
     }
-};
-
-// Values of one step and channel a lane: steps t + 4 q + row, channel c; steps past `to`
-// are read again at the last one.
-template <typename T, int Q> struct Column {
-    T v[Q];
-    __device__ __forceinline__ void load(const SeqRows &r, int64_t z, int c, int row, int64_t t, int64_t to)
-    {
-        const T *p = (const T *)r.p + z * r.stride + c;
-        if (t + 4 * Q <= to) {
-            p += (t + row) * r.ld;
-#pragma unroll
-            for (int q = 0; q < Q; ++q)
-                v[q] = p[4 * q * r.ld];
-        } else {
-#pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const int64_t s = t + 4 * q + row;
-                v[q] = p[(s < to ? s : to - 1) * r.ld];
-            }
-        }
-    }
-};
-
-// B or C of STEPS steps: register k holds steps t + k * 16 / R on, lane j of a row the
-// step j / R and the row's state j % R of them.  Zero past the states' end.
-template <typename T, int R, int STEPS> struct Mixed {
-    static constexpr int PER = ROW / R, REGS = STEPS / PER;
-    T v[REGS];
-    __device__ __forceinline__ void load(const SeqRows &r, int64_t z, int g, int states, int row, int j, int64_t t, int64_t to)
-    {
-        const int n = R * row + j % R;
-        const T *p = (const T *)r.p + z * r.stride + (int64_t)g * states + (n < states ? n : states - 1);
-        if (t + STEPS <= to) {
-            p += (t + j / R) * r.ld;
-#pragma unroll
-            for (int k = 0; k < REGS; ++k)
-                v[k] = p[(int64_t)k * PER * r.ld];
-        } else {
-#pragma unroll
-            for (int k = 0; k < REGS; ++k) {
-                const int64_t s = t + k * PER + j / R;
-                v[k] = p[(s < to ? s : to - 1) * r.ld];
-            }
-        }
-        if (n >= states)
-#pragma unroll
-            for (int k = 0; k < REGS; ++k)
-                v[k] = (T)0.f;
-    }
-    __device__ __forceinline__ float at(int k) const { return (float)v[k]; }
 };
 
 // R states of a lane in an array [.., states]
@@ -245,22 +276,28 @@ struct Maps {
     __device__ __forceinline__ int64_t at(int seg, int64_t z, int c) const { return (seg * a.batch + z) * a.dim + c; }
 };
 
+// A step's length.  (Both forms and a choice: a branch would part the block of steps.)
 template <typename T> __device__ __forceinline__ float step_of(T raw, float bias, bool softplus)
 {
-    const float x = (float)raw + bias;
-    return softplus ? softplus_of(x) : x;
+    const float x = (float)raw + bias, s = softplus_of(x);
+    return softplus ? s : x;
 }
 
 constexpr int FWD_WAVES = 4, STEPS = 16;
+// Of a block of saved states: what the adjoint holds in registers at a time, R * part_steps
+// states a lane, and how many times that.
+constexpr int PARTS = 4;
+template <int R> constexpr int part_steps = WAVE / R;
 
 // ENDS: only walks to the end of a segment from zero and writes its map.
-template <typename T, int R, bool ENDS>
-__global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, float *ws, int block_steps)
+template <typename T, int R, bool ENDS, bool GATED>
+__global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, float *ws)
 {
     constexpr bool FULL = sizeof(T) == 4;
-    constexpr int Q = STEPS / 4, PER = ROW / R;
-    __shared__ float2 s_step[FWD_WAVES][STEPS][ROW];
-    __shared__ vec<float, 4> s_C[ENDS ? 1 : FWD_WAVES][STEPS][R];
+    constexpr int Q = STEPS / 4, PER = ROW / R, REGS = R, BLOCK = PARTS * part_steps<R>;
+    // (two of each: the next block's is written while this one's is read)
+    __shared__ float2 s_step[2][FWD_WAVES][STEPS][ROW];
+    __shared__ vec<float, 4> s_C[2][ENDS ? 1 : FWD_WAVES][STEPS][R];
     Place<R> at;
     if (!at.set(a, p, FWD_WAVES))
         return;
@@ -297,79 +334,159 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, fl
                 h[i] = fmaf(__builtin_amdgcn_exp2f(sum * A2[i]), h[i], q[i]);
         }
     }
+    const auto ru = at.template column<T, STEPS>(a.u), rdelta = at.template column<T, STEPS>(a.delta);
+    const auto rz = at.template column<T, STEPS>(a.z), ry = at.template column<T, STEPS>(a.y);
+    const auto rB = at.template mixed<T, STEPS>(a.B, a.states), rC = at.template mixed<T, STEPS>(a.C, a.states);
+    const bool no_state = at.n0 + j % R >= a.states;
     float total = 0.f;
-    Column<T, Q> u, delta, zz, next_u, next_delta, next_z;
-    Mixed<T, R, STEPS> B, C, next_B, next_C;
-    const auto fetch = [&](int64_t t) {
-        next_u.load(a.u, at.z, at.c, row, t, at.to);
-        next_delta.load(a.delta, at.z, at.c, row, t, at.to);
-        next_B.load(a.B, at.z, at.g, a.states, row, j, t, at.to);
-        if constexpr (!ENDS) {
-            next_C.load(a.C, at.z, at.g, a.states, row, j, t, at.to);
-            if (a.z.p)
-                next_z.load(a.z, at.z, at.c, row, t, at.to);
-        }
+    // of the block that is walked, the one after it, and the one on its way
+    T u[Q], z[Q], next_u[Q], next_z[Q], far_u[Q], far_delta[Q], far_z[Q], far_B[REGS], far_C[REGS];
+    float B[REGS], next_B[REGS];
+    const auto fetch = [&](int t, auto whole) {
+        constexpr bool W = whole;
+        ru.template load<W>(far_u, t, at.to - t);
+        rdelta.template load<W>(far_delta, t, at.to - t);
+        rB.template load<W>(far_B, t, at.to - t);
+        if constexpr (!ENDS)
+            rC.template load<W>(far_C, t, at.to - t);
+        if constexpr (GATED)
+            rz.template load<W>(far_z, t, at.to - t);
     };
-    if (at.from < at.to)
-        fetch(at.from);
-    for (int64_t t = at.from; t < at.to; t += STEPS) {
-        u = next_u, delta = next_delta, B = next_B;
-        if constexpr (!ENDS)
-            C = next_C, zz = next_z;
-        if (t + STEPS < at.to)
-            fetch(t + STEPS);
-        if constexpr (!ENDS)
-            if (a.starts && t % block_steps == 0 && at.real)
-                store_states<R>(a.starts + ((at.z * ((a.len + block_steps - 1) / block_steps) + t / block_steps) * a.dim + at.c) * a.states,
-                                at.n0, a.states, h);
-        wave_sync();
+    // what arrived, into LDS
+    const auto stage = [&](int t, int half, auto whole) {
+        float dt[Q], x[Q];
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            // a step past the end leaves the state as it is
-            const bool counts = t + 4 * q + row < at.to;
-            const float dt = counts ? step_of(delta.v[q], bias, a.softplus) : 0.f;
-            const float x = counts ? dt * (float)u.v[q] : 0.f;
-            s_step[wave][4 * q + row][j] = make_float2(dt, x);
-            if constexpr (ENDS)
-                total += dt;
+            dt[q] = step_of(far_delta[q], bias, a.softplus);
+            x[q] = dt[q] * (float)far_u[q];
         }
-        if constexpr (!ENDS)
+        if (!whole && at.to - t < STEPS) // steps past the end leave the state as it is
 #pragma unroll
-            for (int k = 0; k < Mixed<T, R, STEPS>::REGS; ++k)
-                ((float *)&s_C[wave][k * PER + j / R][0])[R * row + j % R] = C.at(k);
-        wave_sync();
-        float y[4];
-        each<STEPS>([&](auto tt) {
-            constexpr int step = tt;
-            const float2 v = s_step[wave][step][j];
-            vec<float, 4> c[R / 4];
-            if constexpr (!ENDS) {
+            for (int q = 0; q < Q; ++q)
+                if (!ru.inside(q, at.to - t))
+                    dt[q] = x[q] = 0.f;
 #pragma unroll
-                for (int k = 0; k < R / 4; ++k)
-                    c[k] = s_C[wave][step][row * (R / 4) + k];
-                y[step % 4] = 0.f;
-            }
-            const float b = B.at(step / PER);
-            each<R>([&](auto ii) {
-                constexpr int i = ii;
-                const float e = __builtin_amdgcn_exp2f(v.x * A2[i]);
-                h[i] = fmaf(e, h[i], v.y * of_row<step % PER * R + i>(b));
-                if constexpr (!ENDS)
-                    y[step % 4] = fmaf(c[i / 4][i % 4], h[i], y[step % 4]);
-            });
-            if constexpr (!ENDS && step % 4 == 3) {
-                constexpr int q = step / 4;
-                const int64_t mine = t + 4 * q + row;
-                float out = fmaf(D, (float)u.v[q], over_rows(y));
-                if (a.z.p) {
-                    const float gate = (float)zz.v[q];
-                    out *= gate * sigmoid_of<FULL>(gate);
-                }
-                if (mine < at.to && at.real)
-                    ((T *)a.y.p)[at.z * a.y.stride + mine * a.y.ld + at.c] = (T)out;
-            }
-        });
+        for (int q = 0; q < Q; ++q) {
+            s_step[half][wave][4 * q + row][j] = make_float2(dt[q], x[q]);
+            next_u[q] = far_u[q];
+            if constexpr (GATED)
+                next_z[q] = far_z[q];
+            if constexpr (ENDS)
+                total += dt[q];
+        }
+#pragma unroll
+        for (int k = 0; k < REGS; ++k) {
+            next_B[k] = no_state ? 0.f : (float)far_B[k];
+            if constexpr (!ENDS)
+                ((float *)&s_C[half][wave][k * PER + j / R][0])[R * row + j % R] = no_state ? 0.f : (float)far_C[k];
+        }
+    };
+    float *start = nullptr;
+    if (!ENDS && a.starts)
+        start = a.starts + ((at.z * ((a.len + BLOCK - 1) / BLOCK) + at.from / BLOCK) * a.dim + at.c) * a.states;
+    int half = 0;
+    if (at.from < at.to) {
+        fetch(at.from, std::false_type());
+        stage(at.from, 0, std::false_type());
+        if (at.from + STEPS < at.to)
+            fetch(at.from + STEPS, std::false_type());
     }
+    // One block; `whole`: it and the two after it are, so that nothing parts its instructions
+    // (4 x 2048 x 4096 bf16, one wave a SIMD: 245 -> 180 us).
+    const auto walk = [&](int t, auto whole) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            u[q] = next_u[q];
+            if constexpr (GATED)
+                z[q] = next_z[q];
+        }
+#pragma unroll
+        for (int k = 0; k < REGS; ++k)
+            B[k] = next_B[k];
+        if constexpr (!ENDS)
+            if (a.starts && t % BLOCK == 0) {
+                if (at.real)
+                    store_states<R>(start, at.n0, a.states, h);
+                start += a.dim * a.states;
+            }
+        wave_sync();
+        // the steps' operands are read a group ahead of their use
+        constexpr int AHEAD = R > 8 ? 2 : 4;
+        struct {
+            float2 v[AHEAD];
+            vec<float, 4> c[AHEAD][ENDS ? 1 : R / 4];
+        } now, next;
+        const auto read = [&](int step) {
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                next.v[k] = s_step[half][wave][step + k][j];
+                if constexpr (!ENDS) {
+#pragma unroll
+                    for (int i = 0; i < R / 4; ++i)
+                        next.c[k][i] = s_C[half][wave][step + k][row * (R / 4) + i];
+                }
+            }
+        };
+        read(0);
+        if (whole || at.to - t > STEPS) {
+            stage(t + STEPS, half ^ 1, whole);
+            if (whole || at.to - t > 2 * STEPS)
+                fetch(t + 2 * STEPS, whole);
+        }
+        float y[Q][4];
+        each<STEPS / AHEAD>([&](auto gg) {
+            constexpr int g = gg;
+            now = next;
+            if constexpr ((g + 1) * AHEAD < STEPS)
+                read((g + 1) * AHEAD);
+            __builtin_amdgcn_sched_barrier(0); // (the reads stay ahead of a group's work)
+            each<AHEAD>([&](auto kk) {
+                constexpr int k = kk, step = g * AHEAD + k;
+                const float2 v = now.v[k];
+                float sum = 0.f;
+                each<R>([&](auto ii) {
+                    constexpr int i = ii;
+                    const float e = __builtin_amdgcn_exp2f(v.x * A2[i]);
+                    h[i] = fmaf(e, h[i], v.y * of_row<step % PER * R + i>(B[step / PER]));
+                    if constexpr (!ENDS)
+                        sum = i ? fmaf(now.c[k][i / 4][i % 4], h[i], sum) : now.c[k][0][0] * h[0];
+                });
+                y[step / 4][step % 4] = sum;
+            });
+        });
+        if constexpr (!ENDS) {
+            T out[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                float s = fmaf(D, (float)u[q], over_rows(y[q]));
+                if constexpr (GATED) {
+                    const float gate = (float)z[q];
+                    s *= gate * sigmoid_of<FULL>(gate);
+                }
+                out[q] = (T)s;
+            }
+            if (at.real) {
+                if (whole || at.to - t >= STEPS) {
+#pragma unroll
+                    for (int q = 0; q < Q; ++q)
+                        ry.store(t, q, out[q]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < Q; ++q)
+                        if (ry.inside(q, at.to - t))
+                            ry.store(t, q, out[q]);
+                }
+            }
+        }
+        half ^= 1;
+    };
+    int t = at.from;
+    for (; at.to - t >= 4 * STEPS; t += 2 * STEPS) { // (two, so that what is kept for the next need not move)
+        walk(t, std::true_type());
+        walk(t + STEPS, std::true_type());
+    }
+    for (; t < at.to; t += STEPS)
+        walk(t, std::false_type());
     if constexpr (ENDS) {
         total = over_rows(total);
         if (at.real) {
@@ -428,21 +545,14 @@ __global__ void __launch_bounds__(256) k_scan_step(ScanArgs a)
 
 // ----------------------------------------------------------------- adjoint ----
 
-constexpr int BWD_WAVES = 8, PARTS = 4;     // of a block of saved states
-template <int R> constexpr int part_steps = WAVE / R; // T: R * T states of a lane in registers
-
-// Where a workgroup's sums over its channels go: [batch, groups * per_group, len, 2, 4 R]
-template <int R> __device__ __forceinline__ float *sums_at(float *part, const ScanArgs &a, const Plan &p, int64_t z, int64_t t)
-{
-    return part + ((z * p.across + blockIdx.x % p.across) * a.len + t) * (8 * R);
-}
+constexpr int BWD_WAVES = 4;
 
 // ENDS: walks a segment back from mu = 0 and writes its map.
 template <typename T, int R>
 __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan_adjoint_ends(ScanArgs a, Plan p, float *ws)
 {
     constexpr bool FULL = sizeof(T) == 4;
-    constexpr int Q = STEPS / 4, PER = ROW / R;
+    constexpr int Q = STEPS / 4, PER = ROW / R, REGS = R;
     __shared__ float2 s_step[FWD_WAVES][STEPS][ROW];
     Place<R> at;
     if (!at.set(a, p, FWD_WAVES))
@@ -466,29 +576,36 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan_adjoint_ends(ScanArgs 
         return;
     }
     float total = 0.f;
-    Column<T, Q> delta, zz, adj, next_delta, next_z, next_adj;
-    Mixed<T, R, STEPS> C, next_C;
-    const auto fetch = [&](int64_t t) {
-        next_delta.load(a.delta, at.z, at.c, row, t, at.to);
-        next_adj.load(a.adj, at.z, at.c, row, t, at.to);
-        next_C.load(a.C, at.z, at.g, a.states, row, j, t, at.to);
-        if (a.z.p)
-            next_z.load(a.z, at.z, at.c, row, t, at.to);
+    const bool gated = a.z.p, no_state = at.n0 + j % R >= a.states;
+    const auto rdelta = at.template column<T, STEPS>(a.delta), radj = at.template column<T, STEPS>(a.adj);
+    const auto rz = at.template column<T, STEPS>(gated ? a.z : a.adj);
+    const auto rC = at.template mixed<T, STEPS>(a.C, a.states);
+    T delta[Q], z[Q], adj[Q], next_delta[Q], next_z[Q], next_adj[Q], next_C[REGS];
+    const auto fetch = [&](int t) {
+        rdelta.load(next_delta, t, at.to - t);
+        radj.load(next_adj, t, at.to - t);
+        rz.load(next_z, t, at.to - t);
+        rC.load(next_C, t, at.to - t);
     };
-    const int64_t last = at.from + (at.to - 1 - at.from) / STEPS * STEPS;
+    const int last = at.from + (at.to - 1 - at.from) / STEPS * STEPS;
     fetch(last);
-    for (int64_t t = last; t >= at.from; t -= STEPS) {
-        delta = next_delta, adj = next_adj, C = next_C, zz = next_z;
+    for (int t = last; t >= at.from; t -= STEPS) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            delta[q] = next_delta[q], z[q] = next_z[q], adj[q] = next_adj[q];
+        float cc[REGS];
+#pragma unroll
+        for (int k = 0; k < REGS; ++k)
+            cc[k] = no_state ? 0.f : (float)next_C[k];
         if (t > at.from)
             fetch(t - STEPS);
         wave_sync();
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const bool counts = t + 4 * q + row < at.to;
-            float dy = (float)adj.v[q];
-            if (a.z.p)
-                dy *= (float)zz.v[q] * sigmoid_of<FULL>((float)zz.v[q]);
-            const float dt = counts ? step_of(delta.v[q], bias, a.softplus) : 0.f;
+            const bool counts = rdelta.inside(q, at.to - t);
+            const float gate = (float)z[q];
+            const float dy = (float)adj[q] * (gated ? gate * sigmoid_of<FULL>(gate) : 1.f);
+            const float dt = counts ? step_of(delta[q], bias, a.softplus) : 0.f;
             s_step[wave][4 * q + row][j] = make_float2(dt, counts ? dy : 0.f);
             total += dt;
         }
@@ -496,10 +613,9 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan_adjoint_ends(ScanArgs 
         each<STEPS>([&](auto tt) {
             constexpr int step = STEPS - 1 - tt;
             const float2 v = s_step[wave][step][j];
-            const float c = C.at(step / PER);
             each<R>([&](auto ii) {
                 constexpr int i = ii;
-                mu[i] = __builtin_amdgcn_exp2f(v.x * A2[i]) * (mu[i] + v.y * of_row<step % PER * R + i>(c));
+                mu[i] = __builtin_amdgcn_exp2f(v.x * A2[i]) * (mu[i] + v.y * of_row<step % PER * R + i>(cc[step / PER]));
             });
         });
     }
@@ -514,7 +630,7 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan_adjoint_ends(ScanArgs 
 }
 
 template <typename T, int R>
-__global__ void __launch_bounds__(BWD_WAVES *WAVE, 2) k_scan_adjoint(ScanArgs a, Plan p, float *ws, float *sums, float *own)
+__global__ void __launch_bounds__(BWD_WAVES *WAVE) k_scan_adjoint(ScanArgs a, Plan p, float *ws, float *sums, float *own)
 {
     constexpr bool FULL = sizeof(T) == 4;
     constexpr int TS = part_steps<R>, Q = TS / 4, PER = ROW / R, BLOCK = PARTS * TS, REGS = TS / PER;
@@ -555,18 +671,26 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, 2) k_scan_adjoint(ScanArgs a,
 #pragma unroll
         for (int i = 0; i < R; ++i)
             mu[i] = 0.f;
+    const bool gated = a.z.p, no_state = at.n0 + j % R >= a.states;
+    const auto ru = at.template column<T, TS, false>(a.u), rdelta = at.template column<T, TS, false>(a.delta);
+    const auto radj = at.template column<T, TS, false>(a.adj), rz = at.template column<T, TS, false>(gated ? a.z : a.adj);
+    const auto rB = at.template mixed<T, TS, false>(a.B, a.states), rC = at.template mixed<T, TS, false>(a.C, a.states);
+    const auto wu = at.template column<T, TS, false>(a.adj_u), wdelta = at.template column<T, TS, false>(a.adj_delta);
+    const auto wz = at.template column<T, TS, false>(gated ? a.adj_z : a.adj_u);
+    // the workgroup's sums over its channels: [batch, groups * per_group, len, 2, 4 R]
+    sums += (at.z * p.across + blockIdx.x % (unsigned)p.across) * a.len * (8 * R);
     float dD = 0.f, dbias = 0.f;
     int turn = 0;
     const int64_t blocks = (a.len + BLOCK - 1) / BLOCK;
-    const int64_t last = at.from + (at.to - 1 - at.from) / BLOCK * BLOCK;
-    for (int64_t b0 = last; b0 >= at.from; b0 -= BLOCK) {
+    const int last = at.from + (at.to - 1 - at.from) / BLOCK * BLOCK;
+    for (int b0 = last; b0 >= at.from; b0 -= BLOCK) {
         float start[R];
         load_states<R>(a.starts + ((at.z * blocks + b0 / BLOCK) * a.dim + at.c) * a.states, at.n0, a.states, start);
         if (!at.real)
 #pragma unroll
             for (int i = 0; i < R; ++i)
                 start[i] = 0.f;
-        const int parts = (int)((at.to - b0 < BLOCK ? at.to - b0 : BLOCK) + TS - 1) / TS;
+        const int parts = (min(at.to - b0, BLOCK) + TS - 1) / TS;
         // the states that the parts start from
         {
             float h[R];
@@ -574,24 +698,23 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, 2) k_scan_adjoint(ScanArgs a,
             for (int i = 0; i < R; ++i)
                 h[i] = start[i];
             for (int part = 0; part + 1 < parts; ++part) {
-                const int64_t t = b0 + part * TS;
-                Column<T, Q> u, delta;
-                Mixed<T, R, TS> B;
-                u.load(a.u, at.z, at.c, row, t, at.to);
-                delta.load(a.delta, at.z, at.c, row, t, at.to);
-                B.load(a.B, at.z, at.g, a.states, row, j, t, at.to);
+                const int t = b0 + part * TS;
+                T u[Q], delta[Q], B[REGS];
+                ru.load(u, t, TS);
+                rdelta.load(delta, t, TS);
+                rB.load(B, t, TS);
                 wave_sync();
 #pragma unroll
                 for (int q = 0; q < Q; ++q) {
-                    const float dt = at.real ? step_of(delta.v[q], bias, a.softplus) : 0.f;
-                    const vec<float, 4> v = {dt, at.real ? dt * (float)u.v[q] : 0.f, 0.f, 0.f};
+                    const float dt = at.real ? step_of(delta[q], bias, a.softplus) : 0.f;
+                    const vec<float, 4> v = {dt, at.real ? dt * (float)u[q] : 0.f, 0.f, 0.f};
                     s_step[wave][4 * q + row][j] = v;
                 }
                 wave_sync();
                 each<TS>([&](auto tt) {
                     constexpr int step = tt;
                     const vec<float, 4> v = s_step[wave][step][j];
-                    const float bb = B.at(step / PER);
+                    const float bb = no_state ? 0.f : (float)B[step / PER];
                     each<R>([&](auto ii) {
                         constexpr int i = ii;
                         h[i] = fmaf(__builtin_amdgcn_exp2f(v[0] * A2[i]), h[i], v[1] * of_row<step % PER * R + i>(bb));
@@ -605,16 +728,14 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, 2) k_scan_adjoint(ScanArgs a,
             }
         }
         for (int part = parts - 1; part >= 0; --part) {
-            const int64_t t = b0 + part * TS;
-            Column<T, Q> u, delta, zz, adj;
-            Mixed<T, R, TS> B, C;
-            u.load(a.u, at.z, at.c, row, t, at.to);
-            delta.load(a.delta, at.z, at.c, row, t, at.to);
-            adj.load(a.adj, at.z, at.c, row, t, at.to);
-            if (a.z.p)
-                zz.load(a.z, at.z, at.c, row, t, at.to);
-            B.load(a.B, at.z, at.g, a.states, row, j, t, at.to);
-            C.load(a.C, at.z, at.g, a.states, row, j, t, at.to);
+            const int t = b0 + part * TS, left = at.to - t;
+            T u[Q], delta[Q], z[Q], adj[Q], rawB[REGS], rawC[REGS];
+            ru.load(u, t, left);
+            rdelta.load(delta, t, left);
+            radj.load(adj, t, left);
+            rz.load(z, t, left);
+            rB.load(rawB, t, left);
+            rC.load(rawC, t, left);
             float first[R];
 #pragma unroll
             for (int i = 0; i < R; ++i)
@@ -627,26 +748,27 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, 2) k_scan_adjoint(ScanArgs a,
             float dt[Q], dy[Q];
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                const bool counts = t + 4 * q + row < at.to && at.real;
-                dy[q] = (float)adj.v[q];
-                if (a.z.p)
-                    dy[q] *= (float)zz.v[q] * sigmoid_of<FULL>((float)zz.v[q]);
+                const bool counts = ru.inside(q, left) && at.real;
+                const float gate = (float)z[q];
+                dy[q] = (float)adj[q] * (gated ? gate * sigmoid_of<FULL>(gate) : 1.f);
                 dy[q] = counts ? dy[q] : 0.f;
-                dt[q] = counts ? step_of(delta.v[q], bias, a.softplus) : 0.f;
-                const vec<float, 4> v = {dt[q], counts ? dt[q] * (float)u.v[q] : 0.f, dy[q], 0.f};
+                dt[q] = counts ? step_of(delta[q], bias, a.softplus) : 0.f;
+                const vec<float, 4> v = {dt[q], counts ? dt[q] * (float)u[q] : 0.f, dy[q], 0.f};
                 s_step[wave][4 * q + row][j] = v;
             }
+            float B[REGS];
 #pragma unroll
             for (int k = 0; k < REGS; ++k) {
-                ((float *)&s_B[wave][k * PER + j / R][0])[R * row + j % R] = B.at(k);
-                ((float *)&s_C[wave][k * PER + j / R][0])[R * row + j % R] = C.at(k);
+                B[k] = no_state ? 0.f : (float)rawB[k];
+                ((float *)&s_B[wave][k * PER + j / R][0])[R * row + j % R] = B[k];
+                ((float *)&s_C[wave][k * PER + j / R][0])[R * row + j % R] = no_state ? 0.f : (float)rawC[k];
             }
             wave_sync();
             float h[TS][R];
             each<TS>([&](auto tt) {
                 constexpr int step = tt;
                 const vec<float, 4> v = s_step[wave][step][j];
-                const float bb = B.at(step / PER);
+                const float bb = B[step / PER];
                 each<R>([&](auto ii) {
                     constexpr int i = ii;
                     h[step][i] = fmaf(__builtin_amdgcn_exp2f(v[0] * A2[i]), step ? h[step ? step - 1 : 0][i] : first[i],
@@ -701,21 +823,19 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, 2) k_scan_adjoint(ScanArgs a,
                     out[0][q * (R / 4) + reg][lane] = over_lanes(pB, j);
                     out[1][q * (R / 4) + reg][lane] = over_lanes(pC, j);
                 });
-                const float along = over_rows(s1), back = over_rows(s2), v = fmaf(D, (float)u.v[q], over_rows(y));
-                const int64_t mine = t + 4 * q + row;
-                if (mine < at.to && at.real) {
-                    const float x = (float)u.v[q];
+                const float along = over_rows(s1), back = over_rows(s2), v = fmaf(D, (float)u[q], over_rows(y));
+                if (ru.inside(q, left) && at.real) {
+                    const float x = (float)u[q];
                     float ddelta = fmaf(x, along, back);
                     if (a.softplus)
-                        ddelta *= sigmoid_of<true>((float)delta.v[q] + bias);
+                        ddelta *= sigmoid_of<true>((float)delta[q] + bias);
                     dD = fmaf(dy[q], x, dD);
                     dbias += ddelta;
-                    ((T *)a.adj_u.p)[at.z * a.adj_u.stride + mine * a.adj_u.ld + at.c] = (T)fmaf(dt[q], along, D * dy[q]);
-                    ((T *)a.adj_delta.p)[at.z * a.adj_delta.stride + mine * a.adj_delta.ld + at.c] = (T)ddelta;
-                    if (a.z.p) {
-                        const float gate = (float)zz.v[q], sg = sigmoid_of<FULL>(gate);
-                        ((T *)a.adj_z.p)[at.z * a.adj_z.stride + mine * a.adj_z.ld + at.c] =
-                            (T)((float)adj.v[q] * v * (sg * fmaf(gate, 1.f - sg, 1.f)));
+                    wu.store(t, q, (T)fmaf(dt[q], along, D * dy[q]));
+                    wdelta.store(t, q, (T)ddelta);
+                    if (gated) {
+                        const float gate = (float)z[q], sg = sigmoid_of<FULL>(gate);
+                        wz.store(t, q, (T)((float)adj[q] * v * (sg * fmaf(gate, 1.f - sg, 1.f))));
                     }
                 }
             });
@@ -728,9 +848,9 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, 2) k_scan_adjoint(ScanArgs a,
 #pragma unroll
                 for (int w = 0; w < BWD_WAVES; ++w)
                     s += s_sum[turn][w][which][reg][l];
-                const int64_t step = t + reg * PER + l % ROW / R;
+                const int step = t + reg * PER + l % ROW / R;
                 if (step < at.to)
-                    sums_at<R>(sums, a, p, at.z, step)[which * 4 * R + R * (l / ROW) + l % R] = s;
+                    sums[(int64_t)step * (8 * R) + which * 4 * R + R * (l / ROW) + l % R] = s;
             }
             turn ^= 1;
         }
@@ -812,7 +932,7 @@ Plan plan_of(const ScanArgs &a, bool adjoint)
     const int64_t all = a.batch * a.groups * wave_count, blocks = std::max<int64_t>(1, (a.len + block - 1) / block);
     const int64_t want = all >= 768 ? 1 : std::min<int64_t>(blocks, std::min<int64_t>(64, 2048 / all));
     const int64_t each = (blocks + want - 1) / want;
-    p.segment = each * block;
+    p.segment = (int)std::min<int64_t>(each * block, INT32_MAX);
     p.segments = (int)((blocks + each - 1) / each);
     return p;
 }
@@ -903,13 +1023,13 @@ chol_status scan(chol_dtype dt, const ScanArgs &a, void *ws, hipStream_t st)
             const Plan p = plan_of(a, false);
             const dim3 grid((unsigned)(a.batch * p.across * p.segments));
             const auto launch = [&](auto kernel) {
-                hipLaunchKernelGGL(kernel, grid, dim3(FWD_WAVES * WAVE), 0, st, a, p, (float *)ws, scan_block(a.states));
+                hipLaunchKernelGGL(kernel, grid, dim3(FWD_WAVES * WAVE), 0, st, a, p, (float *)ws);
             };
             if (p.segments > 1) {
-                launch(k_scan<T, R, true>);
+                launch(k_scan<T, R, true, false>);
                 CHOL_LAUNCH_CHECK();
             }
-            launch(k_scan<T, R, false>);
+            a.z.p ? launch(k_scan<T, R, false, true>) : launch(k_scan<T, R, false, false>);
             CHOL_LAUNCH_CHECK();
             return CHOL_OK;
         });
