@@ -89,23 +89,36 @@ __device__ __forceinline__ float over_rows(float x)
     const float same[4] = {x, x, x, x};
     return over_rows(same);
 }
-// Lane j of a row gets the sum over the row's lanes of x[j].
-__device__ __forceinline__ float over_lanes(const float (&x)[16], int lane)
+// Lane j of a row gets the sum over the row's lanes of x[j].  Halves of the row, then of
+// those, exchange what they do not keep: x[k] + its exchange goes to all lanes, and that of
+// x[k + 8] (k + 4) over the upper half (the bank mask names groups of four lanes whose
+// result is written).  Written with selections the compiler takes 47 instructions, this 35.
+// An operand of an exchange has to be two instructions old: s_nop 1 sees to it for what
+// comes in, and the order below has it for the rest.
+__device__ __forceinline__ float over_lanes(const float (&in)[16], int lane)
 {
-    const bool far = lane & 8, mid = lane & 4;
-    float a[8], b[4];
+    float x[16];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) // rotated by 8 lanes
-        a[k] = (far ? x[k + 8] : x[k]) + dpp<0x128>(far ? x[k] : x[k + 8]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) // lanes l and l ^ 7, then l and l ^ 3 within fours: l ^ 4 up to the order in a four
-        b[k] = (mid ? a[k + 4] : a[k]) + dpp<0x141>(mid ? a[k] : a[k + 4]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        b[k] += dpp<0x4e>(b[k]); // lanes 2 3 0 1 of the four
-        b[k] += dpp<0xb1>(b[k]); // lanes 1 0 3 2
-    }
-    const float lo = lane & 1 ? b[1] : b[0], hi = lane & 1 ? b[3] : b[2];
+    for (int k = 0; k < 16; ++k)
+        x[k] = in[k];
+#define EXCHANGE(k, from, ctrl, mask) "v_add_f32_dpp %" #k ", %" #from ", %" #from " " ctrl " row_mask:0xf bank_mask:" mask "\n\t"
+#define BOTH(k, far, ctrl, mask) EXCHANGE(k, k, ctrl, "0xf") EXCHANGE(k, far, ctrl, mask)
+#define FAR(k, far) BOTH(k, far, "row_ror:8", "0xc")         // lanes l and l + 8
+#define MID(k, far) BOTH(k, far, "row_half_mirror", "0xa")   // l and l ^ 7
+    asm("s_nop 1\n\t"
+        FAR(0, 8) FAR(1, 9) FAR(2, 10) FAR(3, 11) FAR(4, 12) FAR(5, 13) FAR(6, 14) FAR(7, 15)
+        MID(0, 4) MID(1, 5) MID(2, 6) MID(3, 7)
+        EXCHANGE(0, 0, "quad_perm:[2,3,0,1]", "0xf") EXCHANGE(1, 1, "quad_perm:[2,3,0,1]", "0xf")
+        EXCHANGE(2, 2, "quad_perm:[2,3,0,1]", "0xf") EXCHANGE(3, 3, "quad_perm:[2,3,0,1]", "0xf")
+        EXCHANGE(0, 0, "quad_perm:[1,0,3,2]", "0xf") EXCHANGE(1, 1, "quad_perm:[1,0,3,2]", "0xf")
+        EXCHANGE(2, 2, "quad_perm:[1,0,3,2]", "0xf") EXCHANGE(3, 3, "quad_perm:[1,0,3,2]", "0xf")
+        : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]), "+v"(x[4]), "+v"(x[5]), "+v"(x[6]), "+v"(x[7])
+        : "v"(x[8]), "v"(x[9]), "v"(x[10]), "v"(x[11]), "v"(x[12]), "v"(x[13]), "v"(x[14]), "v"(x[15]));
+#undef MID
+#undef FAR
+#undef BOTH
+#undef EXCHANGE
+    const float lo = lane & 1 ? x[1] : x[0], hi = lane & 1 ? x[3] : x[2];
     return lane & 2 ? hi : lo;
 }
 
@@ -284,17 +297,16 @@ template <typename T> __device__ __forceinline__ float step_of(T raw, float bias
 }
 
 constexpr int FWD_WAVES = 4, STEPS = 16;
-// Of a block of saved states: what the adjoint holds in registers at a time, R * part_steps
-// states a lane, and how many times that.
-constexpr int PARTS = 4;
-template <int R> constexpr int part_steps = WAVE / R;
+// Steps between two saved states, and those that the adjoint holds in registers at a time.
+template <int R> constexpr int block_steps = 256 / R;
+template <int R> constexpr int part_steps = R < 16 ? 32 / R : 4;
 
 // ENDS: only walks to the end of a segment from zero and writes its map.
 template <typename T, int R, bool ENDS, bool GATED>
 __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, float *ws)
 {
     constexpr bool FULL = sizeof(T) == 4;
-    constexpr int Q = STEPS / 4, PER = ROW / R, REGS = R, BLOCK = PARTS * part_steps<R>;
+    constexpr int Q = STEPS / 4, PER = ROW / R, REGS = R, BLOCK = block_steps<R>;
     // (two of each: the next block's is written while this one's is read)
     __shared__ float2 s_step[2][FWD_WAVES][STEPS][ROW];
     __shared__ vec<float, 4> s_C[2][ENDS ? 1 : FWD_WAVES][STEPS][R];
@@ -629,12 +641,12 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan_adjoint_ends(ScanArgs 
     }
 }
 
-template <typename T, int R>
-__global__ void __launch_bounds__(BWD_WAVES *WAVE) k_scan_adjoint(ScanArgs a, Plan p, float *ws, float *sums, float *own)
+template <typename T, int R, bool GATED>
+__global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
+    k_scan_adjoint(ScanArgs a, Plan p, float *ws, float *sums, float *own)
 {
     constexpr bool FULL = sizeof(T) == 4;
-    constexpr int TS = part_steps<R>, Q = TS / 4, PER = ROW / R, BLOCK = PARTS * TS, REGS = TS / PER;
-    static_assert(REGS == 4, "");
+    constexpr int TS = part_steps<R>, Q = TS / 4, PER = ROW / R, REGS = TS / PER, BLOCK = block_steps<R>, PARTS = BLOCK / TS;
     __shared__ vec<float, 4> s_step[BWD_WAVES][TS][ROW];
     __shared__ vec<float, 4> s_B[BWD_WAVES][TS][R], s_C[BWD_WAVES][TS][R];
     __shared__ float s_sum[2][BWD_WAVES][2][REGS][WAVE];
@@ -671,120 +683,164 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE) k_scan_adjoint(ScanArgs a, Pl
 #pragma unroll
         for (int i = 0; i < R; ++i)
             mu[i] = 0.f;
-    const bool gated = a.z.p, no_state = at.n0 + j % R >= a.states;
+    const bool no_state = at.n0 + j % R >= a.states;
     const auto ru = at.template column<T, TS, false>(a.u), rdelta = at.template column<T, TS, false>(a.delta);
-    const auto radj = at.template column<T, TS, false>(a.adj), rz = at.template column<T, TS, false>(gated ? a.z : a.adj);
+    const auto radj = at.template column<T, TS, false>(a.adj), rz = at.template column<T, TS, false>(a.z);
     const auto rB = at.template mixed<T, TS, false>(a.B, a.states), rC = at.template mixed<T, TS, false>(a.C, a.states);
     const auto wu = at.template column<T, TS, false>(a.adj_u), wdelta = at.template column<T, TS, false>(a.adj_delta);
-    const auto wz = at.template column<T, TS, false>(gated ? a.adj_z : a.adj_u);
+    const auto wz = at.template column<T, TS, false>(a.adj_z);
     // the workgroup's sums over its channels: [batch, groups * per_group, len, 2, 4 R]
     sums += (at.z * p.across + blockIdx.x % (unsigned)p.across) * a.len * (8 * R);
     float dD = 0.f, dbias = 0.f;
     int turn = 0;
-    const int64_t blocks = (a.len + BLOCK - 1) / BLOCK;
+    // a part's inputs are on their way while the one before it is walked
+    T far_u[Q], far_delta[Q], far_z[Q], far_adj[Q], far_B[REGS], far_C[REGS];
+    float far_start[R];
+    const auto fetch_start = [&](int t) {
+        load_states<R>(a.starts + ((at.z * ((a.len + BLOCK - 1) / BLOCK) + t / BLOCK) * a.dim + at.c) * a.states, at.n0,
+                       a.states, far_start);
+    };
+    const auto fetch_up = [&](int t) { // (a part that another follows is whole)
+        ru.template load<true>(far_u, t, TS);
+        rdelta.template load<true>(far_delta, t, TS);
+        rB.template load<true>(far_B, t, TS);
+    };
+    const auto fetch_down = [&](int t) {
+        const int left = at.to - t;
+        ru.load(far_u, t, left);
+        rdelta.load(far_delta, t, left);
+        radj.load(far_adj, t, left);
+        if constexpr (GATED)
+            rz.load(far_z, t, left);
+        rB.load(far_B, t, left);
+        rC.load(far_C, t, left);
+    };
     const int last = at.from + (at.to - 1 - at.from) / BLOCK * BLOCK;
+    fetch_start(last);
+    at.to - last > TS ? fetch_up(last) : fetch_down(last);
     for (int b0 = last; b0 >= at.from; b0 -= BLOCK) {
         float start[R];
-        load_states<R>(a.starts + ((at.z * blocks + b0 / BLOCK) * a.dim + at.c) * a.states, at.n0, a.states, start);
-        if (!at.real)
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-                start[i] = 0.f;
+        for (int i = 0; i < R; ++i)
+            start[i] = at.real ? far_start[i] : 0.f;
         const int parts = (min(at.to - b0, BLOCK) + TS - 1) / TS;
         // the states that the parts start from
-        {
-            float h[R];
+        float h0[R];
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-                h[i] = start[i];
-            for (int part = 0; part + 1 < parts; ++part) {
-                const int t = b0 + part * TS;
-                T u[Q], delta[Q], B[REGS];
-                ru.load(u, t, TS);
-                rdelta.load(delta, t, TS);
-                rB.load(B, t, TS);
-                wave_sync();
+        for (int i = 0; i < R; ++i)
+            h0[i] = start[i];
+        for (int part = 0; part + 1 < parts; ++part) {
+            float B[REGS], dt[Q], x[Q];
 #pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    const float dt = at.real ? step_of(delta[q], bias, a.softplus) : 0.f;
-                    const vec<float, 4> v = {dt, at.real ? dt * (float)u[q] : 0.f, 0.f, 0.f};
-                    s_step[wave][4 * q + row][j] = v;
-                }
-                wave_sync();
-                each<TS>([&](auto tt) {
-                    constexpr int step = tt;
-                    const vec<float, 4> v = s_step[wave][step][j];
-                    const float bb = no_state ? 0.f : (float)B[step / PER];
-                    each<R>([&](auto ii) {
-                        constexpr int i = ii;
-                        h[i] = fmaf(__builtin_amdgcn_exp2f(v[0] * A2[i]), h[i], v[1] * of_row<step % PER * R + i>(bb));
-                    });
+            for (int q = 0; q < Q; ++q) {
+                dt[q] = at.real ? step_of(far_delta[q], bias, a.softplus) : 0.f;
+                x[q] = at.real ? dt[q] * (float)far_u[q] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < REGS; ++k)
+                B[k] = no_state ? 0.f : (float)far_B[k];
+            if (part + 2 < parts)
+                fetch_up(b0 + (part + 1) * TS);
+            else
+                fetch_down(b0 + (part + 1) * TS);
+            wave_sync();
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                *(float2 *)&s_step[wave][4 * q + row][j] = make_float2(dt[q], x[q]);
+            wave_sync();
+            float2 v[TS];
+#pragma unroll
+            for (int k = 0; k < TS; ++k)
+                v[k] = *(const float2 *)&s_step[wave][k][j];
+            each<TS>([&](auto tt) {
+                constexpr int step = tt;
+                each<R>([&](auto ii) {
+                    constexpr int i = ii;
+                    h0[i] = fmaf(__builtin_amdgcn_exp2f(v[step].x * A2[i]), h0[i],
+                                 v[step].y * of_row<step % PER * R + i>(B[step / PER]));
                 });
+            });
 #pragma unroll
-                for (int k = 0; k < R / 4; ++k) {
-                    const vec<float, 4> v = {h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]};
-                    s_state[wave][part][k][lane] = v;
-                }
+            for (int k = 0; k < R / 4; ++k) {
+                const vec<float, 4> w = {h0[4 * k], h0[4 * k + 1], h0[4 * k + 2], h0[4 * k + 3]};
+                s_state[wave][part][k][lane] = w;
             }
         }
+        // (the last part starts where that walk ended: h0)
         for (int part = parts - 1; part >= 0; --part) {
             const int t = b0 + part * TS, left = at.to - t;
-            T u[Q], delta[Q], z[Q], adj[Q], rawB[REGS], rawC[REGS];
-            ru.load(u, t, left);
-            rdelta.load(delta, t, left);
-            radj.load(adj, t, left);
-            rz.load(z, t, left);
-            rB.load(rawB, t, left);
-            rC.load(rawC, t, left);
-            float first[R];
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                first[i] = start[i];
-            if (part > 0)
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-                    first[i] = s_state[wave][part - 1][i / 4][lane][i % 4];
-            wave_sync();
-            float dt[Q], dy[Q];
+            float dt[Q], dy[Q], u[Q], raw[Q], slope[Q], B[REGS], C[REGS];
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
                 const bool counts = ru.inside(q, left) && at.real;
-                const float gate = (float)z[q];
-                dy[q] = (float)adj[q] * (gated ? gate * sigmoid_of<FULL>(gate) : 1.f);
-                dy[q] = counts ? dy[q] : 0.f;
-                dt[q] = counts ? step_of(delta[q], bias, a.softplus) : 0.f;
-                const vec<float, 4> v = {dt[q], counts ? dt[q] * (float)u[q] : 0.f, dy[q], 0.f};
-                s_step[wave][4 * q + row][j] = v;
+                u[q] = counts ? (float)far_u[q] : 0.f;
+                raw[q] = (float)far_delta[q] + bias;
+                dt[q] = counts ? step_of(far_delta[q], bias, a.softplus) : 0.f;
+                dy[q] = counts ? (float)far_adj[q] : 0.f;
+                slope[q] = 0.f;
+                if constexpr (GATED) {
+                    const float gate = counts ? (float)far_z[q] : 0.f, sg = sigmoid_of<FULL>(gate);
+                    slope[q] = dy[q] * (sg * fmaf(gate, 1.f - sg, 1.f));
+                    dy[q] *= gate * sg;
+                }
             }
-            float B[REGS];
 #pragma unroll
             for (int k = 0; k < REGS; ++k) {
-                B[k] = no_state ? 0.f : (float)rawB[k];
-                ((float *)&s_B[wave][k * PER + j / R][0])[R * row + j % R] = B[k];
-                ((float *)&s_C[wave][k * PER + j / R][0])[R * row + j % R] = no_state ? 0.f : (float)rawC[k];
+                B[k] = no_state ? 0.f : (float)far_B[k];
+                C[k] = no_state ? 0.f : (float)far_C[k];
             }
-            wave_sync();
-            float h[TS][R];
-            each<TS>([&](auto tt) {
-                constexpr int step = tt;
-                const vec<float, 4> v = s_step[wave][step][j];
-                const float bb = B[step / PER];
-                each<R>([&](auto ii) {
-                    constexpr int i = ii;
-                    h[step][i] = fmaf(__builtin_amdgcn_exp2f(v[0] * A2[i]), step ? h[step ? step - 1 : 0][i] : first[i],
-                                      v[1] * of_row<step % PER * R + i>(bb));
-                });
-            });
-            // the exponentials are formed again: kept, they would take as many registers as h
+            if (part > 0) {
+                fetch_down(t - TS);
+            } else if (b0 > at.from) {
+                fetch_start(b0 - BLOCK);
+                fetch_up(b0 - BLOCK);
+            }
+            float first[R];
 #pragma unroll
             for (int i = 0; i < R; ++i)
-                asm volatile("" : "+v"(A2[i]));
+                first[i] = part == 0 ? start[i] : part == parts - 1 ? h0[i] : s_state[wave][part - 1][i / 4][lane][i % 4];
+            wave_sync();
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const vec<float, 4> v = {dt[q], dt[q] * u[q], dy[q], 0.f};
+                s_step[wave][4 * q + row][j] = v;
+            }
+#pragma unroll
+            for (int k = 0; k < REGS; ++k) {
+                ((float *)&s_B[wave][k * PER + j / R][0])[R * row + j % R] = B[k];
+                ((float *)&s_C[wave][k * PER + j / R][0])[R * row + j % R] = C[k];
+            }
+            wave_sync();
+            // up, keeping the states and (but for many) their exponentials
+            constexpr bool KEEP = R < 16;
+            float h[TS][R], e[KEEP ? TS : 1][R];
+            {
+                float2 v[TS];
+#pragma unroll
+                for (int k = 0; k < TS; ++k)
+                    v[k] = *(const float2 *)&s_step[wave][k][j];
+                each<TS>([&](auto tt) {
+                    constexpr int step = tt;
+                    each<R>([&](auto ii) {
+                        constexpr int i = ii;
+                        const float x = __builtin_amdgcn_exp2f(v[step].x * A2[i]);
+                        if constexpr (KEEP)
+                            e[step][i] = x;
+                        h[step][i] = fmaf(x, step ? h[step ? step - 1 : 0][i] : first[i],
+                                          v[step].y * of_row<step % PER * R + i>(B[step / PER]));
+                    });
+                });
+            }
+            if constexpr (!KEEP)
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    asm volatile("" : "+v"(A2[i])); // (so that the compiler does not keep them either)
+            // and down; a step's operands are on their way while the one after it is walked
             float(*const out)[REGS][WAVE] = s_sum[turn][wave];
-            // a step's operands are on their way while the one after it is walked
             struct {
                 vec<float, 4> v, b[R / 4], c[R / 4];
             } now, next;
-            const auto fetch = [&](int step) {
+            const auto read = [&](int step) {
                 next.v = s_step[wave][step][j];
 #pragma unroll
                 for (int k = 0; k < R / 4; ++k) {
@@ -792,7 +848,8 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE) k_scan_adjoint(ScanArgs a, Pl
                     next.c[k] = s_C[wave][step][row * (R / 4) + k];
                 }
             };
-            fetch(TS - 1);
+            read(TS - 1);
+            T out_u[Q], out_delta[Q], out_z[Q];
             each<Q>([&](auto qq) {
                 constexpr int q = Q - 1 - qq;
                 float y[4] = {}, s1[4] = {}, s2[4] = {};
@@ -803,18 +860,19 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE) k_scan_adjoint(ScanArgs a, Pl
                         constexpr int at_k = PER - 1 - kk, k = reg * PER + at_k, step = 4 * q + k;
                         now = next;
                         if constexpr (step > 0)
-                            fetch(step - 1);
+                            read(step - 1);
                         __builtin_amdgcn_sched_barrier(0);
                         const vec<float, 4> v = now.v;
 #pragma unroll
                         for (int i = 0; i < R; ++i) {
                             const float bb = now.b[i / 4][i % 4], cc = now.c[i / 4][i % 4];
                             const float g = fmaf(cc, v[2], mu[i]);
-                            y[k] = fmaf(cc, h[step][i], y[k]);
+                            if constexpr (GATED)
+                                y[k] = fmaf(cc, h[step][i], y[k]);
                             pC[at_k * R + i] = v[2] * h[step][i];
                             pB[at_k * R + i] = g * v[1];
                             s1[k] = fmaf(g, bb, s1[k]);
-                            mu[i] = g * __builtin_amdgcn_exp2f(v[0] * A2[i]);
+                            mu[i] = g * (KEEP ? e[KEEP ? step : 0][i] : __builtin_amdgcn_exp2f(v[0] * A2[i]));
                             const float w = mu[i] * (step ? h[step ? step - 1 : 0][i] : first[i]);
                             s2[k] = fmaf(A[i], w, s2[k]);
                             dA[i] = fmaf(v[0], w, dA[i]);
@@ -823,25 +881,31 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE) k_scan_adjoint(ScanArgs a, Pl
                     out[0][q * (R / 4) + reg][lane] = over_lanes(pB, j);
                     out[1][q * (R / 4) + reg][lane] = over_lanes(pC, j);
                 });
-                const float along = over_rows(s1), back = over_rows(s2), v = fmaf(D, (float)u[q], over_rows(y));
-                if (ru.inside(q, left) && at.real) {
-                    const float x = (float)u[q];
-                    float ddelta = fmaf(x, along, back);
-                    if (a.softplus)
-                        ddelta *= sigmoid_of<true>((float)delta[q] + bias);
-                    dD = fmaf(dy[q], x, dD);
-                    dbias += ddelta;
-                    wu.store(t, q, (T)fmaf(dt[q], along, D * dy[q]));
-                    wdelta.store(t, q, (T)ddelta);
-                    if (gated) {
-                        const float gate = (float)z[q], sg = sigmoid_of<FULL>(gate);
-                        wz.store(t, q, (T)((float)adj[q] * v * (sg * fmaf(gate, 1.f - sg, 1.f))));
-                    }
-                }
+                const float along = over_rows(s1), back = over_rows(s2);
+                float ddelta = fmaf(u[q], along, back);
+                const float sg = sigmoid_of<true>(raw[q]);
+                ddelta *= a.softplus ? sg : 1.f;
+                dD = fmaf(dy[q], u[q], dD);
+                out_u[q] = (T)fmaf(dt[q], along, D * dy[q]);
+                out_delta[q] = (T)ddelta;
+                if constexpr (GATED)
+                    out_z[q] = (T)(slope[q] * fmaf(D, u[q], over_rows(y)));
+                dbias += ru.inside(q, left) ? ddelta : 0.f;
             });
+            if (at.real) {
+#pragma unroll
+                for (int q = 0; q < Q; ++q)
+                    if (ru.inside(q, left)) {
+                        wu.store(t, q, out_u[q]);
+                        wdelta.store(t, q, out_delta[q]);
+                        if constexpr (GATED)
+                            wz.store(t, q, out_z[q]);
+                    }
+            }
             // (the other half is written while this one is read: a wave reaches the next
             // barrier only after it has read)
             __syncthreads();
+#pragma unroll
             for (int i = threadIdx.x; i < 2 * REGS * WAVE; i += BWD_WAVES * WAVE) {
                 const int which = i / (REGS * WAVE), reg = i / WAVE % REGS, l = i % WAVE;
                 float s = 0.f;
@@ -979,7 +1043,7 @@ bool grid_ok(double threads) { return threads <= 4294967295.0; }
 
 } // namespace
 
-int scan_block(int states) { return PARTS * WAVE / rows_of(states); }
+int scan_block(int states) { return 256 / rows_of(states); }
 
 int64_t scan_workspace(const ScanArgs &a)
 {
@@ -1061,8 +1125,11 @@ chol_status scan_adjoint(chol_dtype dt, const ScanArgs &a, void *ws, hipStream_t
                                    dim3(FWD_WAVES * WAVE), 0, st, a, f, maps);
                 CHOL_LAUNCH_CHECK();
             }
-            hipLaunchKernelGGL((k_scan_adjoint<T, R>), dim3((unsigned)(a.batch * p.across * p.segments)),
-                               dim3(BWD_WAVES * WAVE), 0, st, a, p, maps, sums, own);
+            const auto launch = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, dim3((unsigned)(a.batch * p.across * p.segments)), dim3(BWD_WAVES * WAVE), 0, st,
+                                   a, p, maps, sums, own);
+            };
+            a.z.p ? launch(k_scan_adjoint<T, R, true>) : launch(k_scan_adjoint<T, R, false>);
             CHOL_LAUNCH_CHECK();
             hipLaunchKernelGGL((k_scan_mixed_sums<T>), dim3((unsigned)ceil_of(a.batch * a.len * a.groups * 2 * a.states, 256)),
                                dim3(256), 0, st, a, p, (const float *)sums, 4 * R);
