@@ -287,6 +287,29 @@ struct Maps {
     {
     }
     __device__ __forceinline__ int64_t at(int seg, int64_t z, int c) const { return (seg * a.batch + z) * a.dim + c; }
+    // x through the maps of `count` segments from `seg` on, `step` apart; a few are on
+    // their way together (16384 x 256 bf16 with 64 segments 67 -> 53 us)
+    template <int R>
+    __device__ __forceinline__ void apply(float (&x)[R], int seg, int count, int step, int64_t z, int c, int n0,
+                                          const float (&A2)[R]) const
+    {
+        constexpr int AT_ONCE = 32 / R;
+        for (int s = 0; s < count; s += AT_ONCE) {
+            float total[AT_ONCE], q[AT_ONCE][R];
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k) {
+                const int64_t m = at(seg + (s + k < count ? s + k : count - 1) * step, z, c);
+                total[k] = sum[m];
+                load_states<R>(Q + m * a.states, n0, a.states, q[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k)
+                if (s + k < count)
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        x[i] = fmaf(__builtin_amdgcn_exp2f(total[k] * A2[i]), x[i], q[k][i]);
+        }
+    }
 };
 
 // A step's length.  (Both forms and a choice: a branch would part the block of steps.)
@@ -336,15 +359,7 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, fl
             load_states<R>(maps.Q + maps.at(p.segments - 1, at.z, at.c) * a.states, at.n0, a.states, h);
         else if (a.h0)
             load_states<R>(a.h0 + (at.z * a.dim + at.c) * a.states, at.n0, a.states, h);
-        for (int s = 0; s < at.seg; ++s) {
-            const int64_t m = maps.at(s, at.z, at.c);
-            const float sum = maps.sum[m];
-            float q[R];
-            load_states<R>(maps.Q + m * a.states, at.n0, a.states, q);
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                h[i] = fmaf(__builtin_amdgcn_exp2f(sum * A2[i]), h[i], q[i]);
-        }
+        maps.template apply<R>(h, 0, at.seg, 1, at.z, at.c, at.n0, A2);
     }
     const auto ru = at.template column<T, STEPS>(a.u), rdelta = at.template column<T, STEPS>(a.delta);
     const auto rz = at.template column<T, STEPS>(a.z), ry = at.template column<T, STEPS>(a.y);
@@ -668,15 +683,7 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
     } else {
         const Maps maps(a, ws, p.segments);
         load_states<R>(maps.Q + maps.at(0, at.z, at.c) * a.states, at.n0, a.states, mu);
-        for (int s = p.segments - 1; s > at.seg; --s) {
-            const int64_t m = maps.at(s, at.z, at.c);
-            const float sum = maps.sum[m];
-            float q[R];
-            load_states<R>(maps.Q + m * a.states, at.n0, a.states, q);
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                mu[i] = fmaf(__builtin_amdgcn_exp2f(sum * A2[i]), mu[i], q[i]);
-        }
+        maps.template apply<R>(mu, p.segments - 1, p.segments - 1 - at.seg, -1, at.z, at.c, at.n0, A2);
     }
     // lanes without a channel add nothing to the sums over the channels
     if (!at.real)
@@ -992,9 +999,13 @@ Plan plan_of(const ScanArgs &a, bool adjoint)
     const int64_t per = a.dim / a.groups, wave_count = (per + ROW - 1) / ROW;
     p.per_group = (int)((wave_count + waves - 1) / waves);
     p.across = (int64_t)p.per_group * a.groups;
-    // Segments cost each step about as much again.
+    // A first walk costs a step of the forward about as much again, and half as much of the
+    // adjoint, which also needs two waves a SIMD more: 4 x 2048 x 4096 bf16 (1024 waves, one a
+    // SIMD) forward 178 us whole, 219 in 4 segments, adjoint 900 and 721; 2 x 2048 x 4096 forward
+    // 160 in 2 segments, 126 in 8, adjoint 576 and 368.  More than 64 cost more to put
+    // together than they save (16384 x 256 forward 68 us, with 256 116).
     const int64_t all = a.batch * a.groups * wave_count, blocks = std::max<int64_t>(1, (a.len + block - 1) / block);
-    const int64_t want = all >= 768 ? 1 : std::min<int64_t>(blocks, std::min<int64_t>(64, 2048 / all));
+    const int64_t want = all >= (adjoint ? 1536 : 768) ? 1 : std::min<int64_t>({blocks, 64, 4096 / all});
     const int64_t each = (blocks + want - 1) / want;
     p.segment = (int)std::min<int64_t>(each * block, INT32_MAX);
     p.segments = (int)((blocks + each - 1) / each);
