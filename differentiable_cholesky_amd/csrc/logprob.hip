@@ -23,6 +23,7 @@
 #include "../../include/libchol.h"
 #include "logprob.hpp"
 #include "rows.hpp"
+#include "wave.hpp"
 
 namespace chol {
 
@@ -44,31 +45,19 @@ __device__ __forceinline__ float value_of(int key) { return __int_as_float(key ^
 
 __device__ __forceinline__ float wave_max(float x)
 {
-#pragma unroll
-    for (int o = WAVE / 2; o > 0; o /= 2)
-        x = fmaxf(x, __shfl_xor(x, o));
-    return x;
+    return over_wave(x, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float wave_sum(float x)
 {
-#pragma unroll
-    for (int o = WAVE / 2; o > 0; o /= 2)
-        x += __shfl_xor(x, o);
-    return x;
+    return over_wave(x, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ int wave_max(int x)
 {
-#pragma unroll
-    for (int o = WAVE / 2; o > 0; o /= 2)
-        x = max(x, __shfl_xor(x, o));
-    return x;
+    return over_wave(x, [](int a, int b) { return max(a, b); });
 }
 __device__ __forceinline__ int wave_min(int x)
 {
-#pragma unroll
-    for (int o = WAVE / 2; o > 0; o /= 2)
-        x = min(x, __shfl_xor(x, o));
-    return x;
+    return over_wave(x, [](int a, int b) { return min(a, b); });
 }
 
 struct Entry {
@@ -190,9 +179,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
                     count += __popcll(who);
                 }
             }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        wave_sync();
         if (count <= WAVE) {
             Entry e{NONE, INT_MAX};
             if (lane < count)
@@ -245,9 +232,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
             }
         }
     } else {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        wave_sync();
     }
     if (lane == 0) {
         if (chunks > 1)
@@ -257,41 +242,47 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
     }
     if constexpr (TOP) {
         const float lse = all.m == -INFINITY ? -INFINITY : fmaf(a.scale, all.m, __builtin_amdgcn_logf(all.s) * LN2);
-        // the waves' lists, a lane its place in one of them; TEAM * top entries
-        int at = 0;
-        for (int r = 0; r < a.top; ++r) {
-            Entry f;
-            if constexpr (TEAM == 1) {
-                f = s_list[wave][r];
-            } else {
-                Entry e{NONE, INT_MAX};
-                if (lane < TEAM && at < a.top)
-                    e = s_list[lane][at];
-                f = wave_first(e);
-                if (lane < TEAM && e.key == f.key && e.index == f.index)
+        // the waves' lists, a lane its place in one of them; lane r keeps the r-th
+        Entry mine{NONE, INT_MAX};
+        if constexpr (TEAM == 1) {
+            if (lane < a.top)
+                mine = s_list[wave][lane];
+        } else {
+            int at = 0;
+            Entry e{NONE, INT_MAX};
+            if (lane < TEAM)
+                e = s_list[lane][0];
+            for (int r = 0; r < a.top; ++r) {
+                const Entry f = wave_first(e);
+                if (lane < TEAM && e.key == f.key && e.index == f.index) {
                     ++at;
-            }
-            if (lane == 0) {
-                if (chunks > 1) {
-                    lists[unit * a.top + r] = f;
-                } else {
-                    const float x = value_of(f.key);
-                    a.top_ids[row * a.top + r] = f.index;
-                    a.top_logp[row * a.top + r] = x == -INFINITY && all.s == all.s ? x : fmaf(a.scale, x, -lse);
+                    e = at < a.top ? s_list[lane][at] : Entry{NONE, INT_MAX};
                 }
+                if (lane == r)
+                    mine = f;
+            }
+        }
+        if (lane < a.top) {
+            if (chunks > 1) {
+                lists[unit * a.top + lane] = mine;
+            } else {
+                const float x = value_of(mine.key);
+                a.top_ids[row * a.top + lane] = mine.index;
+                a.top_logp[row * a.top + lane] = x == -INFINITY && all.s == all.s ? x : fmaf(a.scale, x, -lse);
             }
         }
     }
 }
 
-// Joins a row's chunks, a lane each.
+// Joins a row's chunks, a lane each; one wave.  The lists come to LDS together.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) k_logprob_join(LogprobArgs a, int chunks, const Stats *stats, const Entry *lists)
+__global__ void __launch_bounds__(WAVE) k_logprob_join(LogprobArgs a, int chunks, const Stats *stats, const Entry *lists)
 {
-    const int lane = threadIdx.x % WAVE;
-    const int64_t row = (int64_t)blockIdx.x * WAVES + threadIdx.x / WAVE;
-    if (row >= a.rows)
-        return;
+    extern __shared__ Entry s_lists[];
+    const int lane = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    for (int i = lane; i < chunks * a.top; i += WAVE)
+        s_lists[i] = lists[row * chunks * a.top + i];
     const float k2 = a.scale * LOG2E, given = given_logit<T>(a, row);
     Stats st{-INFINITY, 0.f, 0.f};
     if (lane < chunks)
@@ -307,23 +298,26 @@ __global__ void __launch_bounds__(THREADS) k_logprob_join(LogprobArgs a, int chu
     all.s = wave_sum(s), all.t = wave_sum(t);
     if (lane == 0)
         finish(a, row, all, a.x, given);
+    if (a.top == 0)
+        return;
+    wave_sync();
     const float lse = all.m == -INFINITY ? -INFINITY : fmaf(a.scale, all.m, __builtin_amdgcn_logf(all.s) * LN2);
-    const Entry *list = lists + (row * chunks + lane) * a.top;
+    const Entry *list = s_lists + lane * a.top;
     int at = 0;
-    Entry e{NONE, INT_MAX};
-    if (lane < chunks && a.top > 0)
-        e = list[0];
+    Entry mine{NONE, INT_MAX}, e = lane < chunks ? list[0] : mine;
     for (int r = 0; r < a.top; ++r) {
         const Entry f = wave_first(e);
         if (e.key == f.key && e.index == f.index) {
             ++at;
             e = at < a.top ? list[at] : Entry{NONE, INT_MAX};
         }
-        if (lane == 0) {
-            const float x = value_of(f.key);
-            a.top_ids[row * a.top + r] = f.index;
-            a.top_logp[row * a.top + r] = x == -INFINITY && all.s == all.s ? x : fmaf(a.scale, x, -lse);
-        }
+        if (lane == r)
+            mine = f;
+    }
+    if (lane < a.top) {
+        const float x = value_of(mine.key);
+        a.top_ids[row * a.top + lane] = mine.index;
+        a.top_logp[row * a.top + lane] = x == -INFINITY && all.s == all.s ? x : fmaf(a.scale, x, -lse);
     }
 }
 
@@ -430,8 +424,8 @@ chol_status logprob(chol_dtype dt, const LogprobArgs &a, void *ws, hipStream_t s
             p.vectors == 2 ? with_top(Two(), All()) : with_top(Eight(), All());
         CHOL_LAUNCH_CHECK();
         if (p.chunks > 1) {
-            hipLaunchKernelGGL(k_logprob_join<T>, dim3((unsigned)ceil_of(a.rows, WAVES)), dim3(THREADS), 0, st, a, p.chunks,
-                               (const Stats *)stats, (const Entry *)lists);
+            hipLaunchKernelGGL(k_logprob_join<T>, dim3((unsigned)a.rows), dim3(WAVE), p.chunks * a.top * sizeof(Entry), st, a,
+                               p.chunks, (const Stats *)stats, (const Entry *)lists);
             CHOL_LAUNCH_CHECK();
         }
         return CHOL_OK;

@@ -37,6 +37,7 @@
 #include <utility>
 
 #include "scan.hpp"
+#include "wave.hpp"
 
 namespace chol {
 
@@ -54,33 +55,11 @@ template <int N, typename F> __device__ __forceinline__ void each(F f)
     each_of(f, std::make_integer_sequence<int, N>());
 }
 
-template <int CTRL> __device__ __forceinline__ float dpp(float x)
-{
-    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
-}
-// lane K of the lane's row
-template <int K> __device__ __forceinline__ float of_row(float x) { return dpp<0x150 + K>(x); }
-
-struct Two {
-    float a, b;
-};
-__device__ __forceinline__ Two swap_halves(float x, float y)
-{
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
-    const unsigned p = r[0], q = r[1];
-    return {__uint_as_float(p), __uint_as_float(q)};
-}
-__device__ __forceinline__ Two swap_rows(float x, float y)
-{
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
-    const unsigned p = r[0], q = r[1];
-    return {__uint_as_float(p), __uint_as_float(q)};
-}
 // Row r gets the sum over the four rows of x[r].
 __device__ __forceinline__ float over_rows(const float (&x)[4])
 {
-    const Two p = swap_halves(x[0], x[2]), q = swap_halves(x[1], x[3]);
-    const Two s = swap_rows(p.a + p.b, q.a + q.b);
+    const Two<float> p = swap_halves(x[0], x[2]), q = swap_halves(x[1], x[3]);
+    const Two<float> s = swap_rows(p.a + p.b, q.a + q.b);
     return s.a + s.b;
 }
 // The sum over the rows, in every lane.
@@ -120,15 +99,6 @@ __device__ __forceinline__ float over_lanes(const float (&in)[16], int lane)
 #undef EXCHANGE
     const float lo = lane & 1 ? x[1] : x[0], hi = lane & 1 ? x[3] : x[2];
     return lane & 2 ? hi : lo;
-}
-
-// LDS written by lanes of a wave and read by others of the same wave, whose operations
-// on it are in order.
-__device__ __forceinline__ void wave_sync()
-{
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // log(1 + exp(x)): the larger of x and 0, and log(1 + w) with w = exp(-|x|).  Where
