@@ -12,10 +12,12 @@
 // them) are joined by a second launch, one wave a row.
 //
 // Alternatives: a wave's k-th largest maximum of a lane is a bound that k elements reach,
-// so elements below it are out; those that remain, hardly more than k, are ranked one
-// after the other.  Where more remain than a wave holds (equal values, sorted rows) the
-// wave finds each in turn among its registers, k times the comparisons.  Order: by value,
-// then by the lower index; NaN before all.
+// so only lanes that reach it, hardly more than k, can hold one.  Their elements go through
+// LDS, a lane an element; those that reach the bound are ranked one after the other
+// (4096 x 128000 bf16, 8 alternatives 288 us; comparing every element in its own lane took
+// 896).  Where lanes or elements are too many (equal values, sorted rows) the wave finds each
+// alternative in turn among its registers, k times the comparisons.  Order: by value, then by
+// the lower index; NaN before all.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -32,6 +34,7 @@ namespace {
 constexpr int WAVE = 64, THREADS = 256, WAVES = THREADS / WAVE;
 constexpr int MOST_CHUNKS = WAVE; // a lane each when they are joined
 constexpr int NONE = INT_MIN;     // below the key of any value
+constexpr int SLOTS = 32;         // lanes whose elements are looked at
 
 template <typename T> constexpr int vec_of = 16 / (int)sizeof(T);
 
@@ -62,6 +65,7 @@ __device__ __forceinline__ int wave_min(int x)
 
 struct Entry {
     int key, index;
+    __device__ __forceinline__ bool after(const Entry &o) const { return o.key > key || (o.key == key && o.index < index); }
 };
 
 // The first of the lanes' entries, in every lane; NONE if there is none.
@@ -104,6 +108,9 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
     constexpr int V = vec_of<T>, LANES = TEAM * WAVE, N = NV * V, MOST = CHOL_LOGPROB_MAX_TOP;
     __shared__ Stats s_stats[WAVES];
     __shared__ Entry s_some[TOP ? WAVES : 1][WAVE], s_list[TOP ? WAVES : 1][MOST];
+    __shared__ vec<T, V> s_lane[TOP ? WAVES : 1][SLOTS][NV];
+    __shared__ int s_column[TOP ? WAVES : 1][SLOTS];
+    __shared__ alignas(16) float s_max[TOP ? WAVES : 1][WAVE];
     const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE, t = threadIdx.x % LANES;
     const int64_t unit = (int64_t)blockIdx.x * (WAVES / TEAM) + (TEAM == 1 ? wave : 0);
     if (unit >= a.rows * chunks) // (waves of their own where TEAM is 1)
@@ -130,6 +137,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
 #pragma unroll
         for (int v = 0; v < V; ++v)
             m = fmaxf(m, (float)x[i][v]);
+    const float lane_max = m;
     m = wave_max(m);
     const float ref = m == -INFINITY ? 0.f : m;
     float s = 0.f, w = 0.f;
@@ -141,69 +149,75 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
             s += e;
             w = fmaf(fmaxf(d, -1e30f), e, w); // (e is 0 at -inf)
         }
+    const float lane_sum = s;
     s = wave_sum(s), w = wave_sum(w);
     const Stats mine{m, s, w};
 
     if constexpr (TOP) {
         const int top = a.top;
-        const auto key_at = [&](int i, int v) {
-            const int c = c0 + (i * LANES + t) * V + v;
-            return c < end ? key_of((float)x[i][v]) : NONE;
-        };
-        // the bound
-        int best = NONE;
+        // lanes with fewer than k maxima above their own hold the k-th largest or more
+        s_max[wave][lane] = lane_max;
+        wave_sync();
+        int above = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int l = 0; l < WAVE; l += 4) {
+            const vec<float, 4> other = *(const vec<float, 4> *)&s_max[wave][l];
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                best = max(best, key_at(i, v));
-        int bound = NONE;
-        for (int r = 0; r < top; ++r) {
-            bound = wave_max(best);
-            const uint64_t who = __ballot(best == bound);
-            if (lane == __ffsll((unsigned long long)who) - 1)
-                best = NONE;
+            for (int k = 0; k < 4; ++k)
+                above += other[k] > lane_max ? 1 : 0;
         }
-        bound = max(bound, NONE + 1);
+        const float bound = -wave_max(above < top ? -lane_max : -INFINITY);
+        // (a NaN makes its lane's sum one)
+        const bool holds = above < top || lane_sum != lane_sum;
+        const uint64_t holders = __ballot(holds);
+        const int slots = __popcll(holders);
+        const int slot = __builtin_amdgcn_mbcnt_hi((unsigned)(holders >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)holders, 0));
         int count = 0;
+        if (slots <= SLOTS) {
+            if (holds) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int key = key_at(i, v);
-                const uint64_t who = __ballot(key >= bound);
-                if (who) {
-                    const int at = count + __builtin_amdgcn_mbcnt_hi((unsigned)(who >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)who, 0));
-                    if (key >= bound && at < WAVE)
-                        s_some[wave][at] = {key, c0 + (i * LANES + t) * V + v};
-                    count += __popcll(who);
-                }
+                for (int i = 0; i < NV; ++i)
+                    s_lane[wave][slot][i] = x[i];
+                s_column[wave][slot] = c0 + t * V;
             }
+            wave_sync();
+            for (int at = lane; at - lane < slots * N; at += WAVE) {
+                const int from = at / N, k = at % N, c = from < slots ? s_column[wave][from] + k / V * (LANES * V) + k % V : end;
+                const float y = from < slots ? (float)s_lane[wave][from][k / V][k % V] : -INFINITY;
+                const uint64_t who = __ballot(!(y < bound) && c < end);
+                const int place = count + __builtin_amdgcn_mbcnt_hi((unsigned)(who >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)who, 0));
+                if ((who >> lane & 1) && place < WAVE)
+                    s_some[wave][place] = {key_of(y), c};
+                count += __popcll(who);
+            }
+        } else {
+            count = WAVE + 1;
+        }
         wave_sync();
         if (count <= WAVE) {
+            // a lane's place is the number of those before it
             Entry e{NONE, INT_MAX};
             if (lane < count)
                 e = s_some[wave][lane];
-            for (int r = 0; r < top; ++r) {
-                const Entry f = wave_first(e);
-                if (e.key == f.key && e.index == f.index)
-                    e.key = NONE;
-                if (lane == 0)
-                    s_list[wave][r] = f;
-            }
+            int before = 0;
+            for (int l = 0; l < count; ++l)
+                before += e.after(s_some[wave][l]) ? 1 : 0;
+            if (lane < top)
+                s_list[wave][lane] = {NONE, INT_MAX};
+            if (lane < count && before < top)
+                s_list[wave][before] = e;
         } else {
+            // (from memory again: from registers it would be as many instructions as elements)
             Entry last{INT_MAX, -1};
             for (int r = 0; r < top; ++r) {
                 Entry e{NONE, INT_MAX};
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) { // (columns rise, so the first of equal ones stays)
-                        const int key = key_at(i, v), c = c0 + (i * LANES + t) * V + v;
-                        const bool after = key < last.key || (key == last.key && c > last.index);
-                        if (after && key > e.key)
-                            e = {key, c};
-                    }
+#pragma unroll 1
+                for (int k = 0; k < N; ++k) {
+                    const int c = c0 + (k / V * LANES + t) * V + k % V;
+                    const Entry o{c < end ? key_of((float)p[c]) : NONE, c};
+                    if (o.after(last) && e.after(o))
+                        e = o;
+                }
                 last = wave_first(e);
                 if (lane == 0)
                     s_list[wave][r] = last;
@@ -242,25 +256,39 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
     }
     if constexpr (TOP) {
         const float lse = all.m == -INFINITY ? -INFINITY : fmaf(a.scale, all.m, __builtin_amdgcn_logf(all.s) * LN2);
-        // the waves' lists, a lane its place in one of them; lane r keeps the r-th
+        // The waves' lists together: an entry's place is its own and, in each other list, the
+        // number of those before it (found by halving; entries that are none come last)
         Entry mine{NONE, INT_MAX};
         if constexpr (TEAM == 1) {
             if (lane < a.top)
                 mine = s_list[wave][lane];
         } else {
-            int at = 0;
-            Entry e{NONE, INT_MAX};
-            if (lane < TEAM)
-                e = s_list[lane][0];
-            for (int r = 0; r < a.top; ++r) {
-                const Entry f = wave_first(e);
-                if (lane < TEAM && e.key == f.key && e.index == f.index) {
-                    ++at;
-                    e = at < a.top ? s_list[lane][at] : Entry{NONE, INT_MAX};
+            if (lane < a.top)
+                s_some[0][lane] = mine;
+            wave_sync();
+            for (int at = lane; at < TEAM * a.top; at += WAVE) {
+                const int own = at / a.top;
+                const Entry e = s_list[own][at % a.top];
+                int place = at % a.top;
+#pragma unroll
+                for (int w = 1; w < TEAM; ++w) {
+                    const Entry *const list = s_list[(own + w) % TEAM];
+                    int first = 0;
+                    for (int size = a.top; size > 0; size /= 2) {
+                        // the first of `size + 1` places from `first` on whose entry is not before e
+                        const int half = first + size / 2;
+                        const bool before = e.after(list[half]);
+                        first = before ? half + 1 : first;
+                        size -= before && size % 2 == 0 ? 1 : 0;
+                    }
+                    place += first;
                 }
-                if (lane == r)
-                    mine = f;
+                if (place < a.top && e.key != NONE)
+                    s_some[0][place] = e;
             }
+            wave_sync();
+            if (lane < a.top)
+                mine = s_some[0][lane];
         }
         if (lane < a.top) {
             if (chunks > 1) {
