@@ -296,13 +296,13 @@ template <int R> constexpr int part_steps = R < 16 ? 32 / R : 4;
 
 // ENDS: only walks to the end of a segment from zero and writes its map.
 template <typename T, int R, bool ENDS, bool GATED>
-__global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, float *ws)
+__global__ void __launch_bounds__(FWD_WAVES *WAVE, R > 4 ? 1 : 3) k_scan(ScanArgs a, Plan p, float *ws)
 {
     constexpr bool FULL = sizeof(T) == 4;
     constexpr int Q = STEPS / 4, PER = ROW / R, REGS = R, BLOCK = block_steps<R>;
     // (two of each: the next block's is written while this one's is read)
     __shared__ float2 s_step[2][FWD_WAVES][STEPS][ROW];
-    __shared__ vec<float, 4> s_C[2][ENDS ? 1 : FWD_WAVES][STEPS][R];
+    __shared__ vec<float, 4> s_mixed[2][FWD_WAVES][STEPS][R]; // C; on a first walk B
     Place<R> at;
     if (!at.set(a, p, FWD_WAVES))
         return;
@@ -374,8 +374,7 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, fl
 #pragma unroll
         for (int k = 0; k < REGS; ++k) {
             next_B[k] = no_state ? 0.f : (float)far_B[k];
-            if constexpr (!ENDS)
-                ((float *)&s_C[half][wave][k * PER + j / R][0])[R * row + j % R] = no_state ? 0.f : (float)far_C[k];
+            ((float *)&s_mixed[half][wave][k * PER + j / R][0])[R * row + j % R] = ENDS ? next_B[k] : no_state ? 0.f : (float)far_C[k];
         }
     };
     float *start = nullptr;
@@ -411,17 +410,15 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, fl
         constexpr int AHEAD = R > 8 ? 2 : 4;
         struct {
             float2 v[AHEAD];
-            vec<float, 4> c[AHEAD][ENDS ? 1 : R / 4];
+            vec<float, 4> c[AHEAD][R / 4];
         } now, next;
         const auto read = [&](int step) {
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
                 next.v[k] = s_step[half][wave][step + k][j];
-                if constexpr (!ENDS) {
 #pragma unroll
-                    for (int i = 0; i < R / 4; ++i)
-                        next.c[k][i] = s_C[half][wave][step + k][row * (R / 4) + i];
-                }
+                for (int i = 0; i < R / 4; ++i)
+                    next.c[k][i] = s_mixed[half][wave][step + k][row * (R / 4) + i];
             }
         };
         read(0);
@@ -444,7 +441,10 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, fl
                 each<R>([&](auto ii) {
                     constexpr int i = ii;
                     const float e = __builtin_amdgcn_exp2f(v.x * A2[i]);
-                    h[i] = fmaf(e, h[i], v.y * of_row<step % PER * R + i>(B[step / PER]));
+                    if constexpr (ENDS)
+                        h[i] = fmaf(e, h[i], v.y * now.c[k][i / 4][i % 4]);
+                    else
+                        h[i] = fmaf(e, h[i], v.y * of_row<step % PER * R + i>(B[step / PER]));
                     if constexpr (!ENDS)
                         sum = i ? fmaf(now.c[k][i / 4][i % 4], h[i], sum) : now.c[k][0][0] * h[0];
                 });
@@ -478,10 +478,14 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan(ScanArgs a, Plan p, fl
         half ^= 1;
     };
     int t = at.from;
-    for (; at.to - t >= 4 * STEPS; t += 2 * STEPS) { // (two, so that what is kept for the next need not move)
-        walk(t, std::true_type());
-        walk(t + STEPS, std::true_type());
-    }
+    if constexpr (ENDS)
+        for (; at.to - t >= 3 * STEPS; t += STEPS)
+            walk(t, std::true_type());
+    else
+        for (; at.to - t >= 4 * STEPS; t += 2 * STEPS) { // (two, so that what is kept for the next need not move)
+            walk(t, std::true_type());
+            walk(t + STEPS, std::true_type());
+        }
     for (; t < at.to; t += STEPS)
         walk(t, std::false_type());
     if constexpr (ENDS) {
@@ -550,7 +554,8 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan_adjoint_ends(ScanArgs 
 {
     constexpr bool FULL = sizeof(T) == 4;
     constexpr int Q = STEPS / 4, PER = ROW / R, REGS = R;
-    __shared__ float2 s_step[FWD_WAVES][STEPS][ROW];
+    __shared__ float2 s_step[2][FWD_WAVES][STEPS][ROW];
+    __shared__ vec<float, 4> s_C[2][FWD_WAVES][STEPS][R];
     Place<R> at;
     if (!at.set(a, p, FWD_WAVES))
         return;
@@ -577,43 +582,69 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan_adjoint_ends(ScanArgs 
     const auto rdelta = at.template column<T, STEPS>(a.delta), radj = at.template column<T, STEPS>(a.adj);
     const auto rz = at.template column<T, STEPS>(gated ? a.z : a.adj);
     const auto rC = at.template mixed<T, STEPS>(a.C, a.states);
-    T delta[Q], z[Q], adj[Q], next_delta[Q], next_z[Q], next_adj[Q], next_C[REGS];
-    const auto fetch = [&](int t) {
-        rdelta.load(next_delta, t, at.to - t);
-        radj.load(next_adj, t, at.to - t);
-        rz.load(next_z, t, at.to - t);
-        rC.load(next_C, t, at.to - t);
+    T far_delta[Q], far_z[Q], far_adj[Q], far_C[REGS];
+    const auto fetch = [&](int t, auto whole) {
+        constexpr bool W = whole;
+        rdelta.template load<W>(far_delta, t, at.to - t);
+        radj.template load<W>(far_adj, t, at.to - t);
+        rz.template load<W>(far_z, t, at.to - t);
+        rC.template load<W>(far_C, t, at.to - t);
     };
-    const int last = at.from + (at.to - 1 - at.from) / STEPS * STEPS;
-    fetch(last);
-    for (int t = last; t >= at.from; t -= STEPS) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            delta[q] = next_delta[q], z[q] = next_z[q], adj[q] = next_adj[q];
-        float cc[REGS];
-#pragma unroll
-        for (int k = 0; k < REGS; ++k)
-            cc[k] = no_state ? 0.f : (float)next_C[k];
-        if (t > at.from)
-            fetch(t - STEPS);
-        wave_sync();
+    // what arrived, into LDS; steps past the end leave mu as it is
+    const auto stage = [&](int t, int half) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const bool counts = rdelta.inside(q, at.to - t);
-            const float gate = (float)z[q];
-            const float dy = (float)adj[q] * (gated ? gate * sigmoid_of<FULL>(gate) : 1.f);
-            const float dt = counts ? step_of(delta[q], bias, a.softplus) : 0.f;
-            s_step[wave][4 * q + row][j] = make_float2(dt, counts ? dy : 0.f);
+            const float gate = (float)far_z[q], sg = sigmoid_of<FULL>(gate);
+            const float dy = (float)far_adj[q] * (gated ? gate * sg : 1.f);
+            const float dt = counts ? step_of(far_delta[q], bias, a.softplus) : 0.f;
+            s_step[half][wave][4 * q + row][j] = make_float2(dt, counts ? dy : 0.f);
             total += dt;
         }
+#pragma unroll
+        for (int k = 0; k < REGS; ++k)
+            ((float *)&s_C[half][wave][k * PER + j / R][0])[R * row + j % R] = no_state ? 0.f : (float)far_C[k];
+    };
+    int half = 0;
+    const int last = at.from + (at.to - 1 - at.from) / STEPS * STEPS;
+    fetch(last, std::false_type());
+    stage(last, 0);
+    if (last > at.from)
+        fetch(last - STEPS, std::true_type());
+    for (int t = last; t >= at.from; t -= STEPS, half ^= 1) {
         wave_sync();
-        each<STEPS>([&](auto tt) {
-            constexpr int step = STEPS - 1 - tt;
-            const float2 v = s_step[wave][step][j];
-            each<R>([&](auto ii) {
-                constexpr int i = ii;
-                mu[i] = __builtin_amdgcn_exp2f(v.x * A2[i]) * (mu[i] + v.y * of_row<step % PER * R + i>(cc[step / PER]));
-            });
+        // the steps' operands are read a group ahead of their use
+        constexpr int AHEAD = R > 8 ? 2 : 4;
+        struct {
+            float2 v[AHEAD];
+            vec<float, 4> c[AHEAD][R / 4];
+        } now, next;
+        const auto read = [&](int step) { // and those before it
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                next.v[k] = s_step[half][wave][step - k][j];
+#pragma unroll
+                for (int i = 0; i < R / 4; ++i)
+                    next.c[k][i] = s_C[half][wave][step - k][row * (R / 4) + i];
+            }
+        };
+        read(STEPS - 1);
+        if (t > at.from) {
+            stage(t - STEPS, half ^ 1);
+            if (t - STEPS > at.from)
+                fetch(t - 2 * STEPS, std::true_type());
+        }
+        each<STEPS / AHEAD>([&](auto gg) {
+            constexpr int g = gg;
+            now = next;
+            if constexpr ((g + 1) * AHEAD < STEPS)
+                read(STEPS - 1 - (g + 1) * AHEAD);
+            __builtin_amdgcn_sched_barrier(0); // (the reads stay ahead of a group's work)
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    mu[i] = __builtin_amdgcn_exp2f(now.v[k].x * A2[i]) * fmaf(now.c[k][i / 4][i % 4], now.v[k].y, mu[i]);
         });
     }
     total = over_rows(total);
@@ -636,6 +667,7 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
     __shared__ vec<float, 4> s_B[BWD_WAVES][TS][R], s_C[BWD_WAVES][TS][R];
     __shared__ float s_sum[2][BWD_WAVES][2][REGS][WAVE];
     __shared__ vec<float, 4> s_state[BWD_WAVES][PARTS - 1][R / 4][WAVE];
+    __shared__ float2 s_up[BWD_WAVES][PARTS - 1][TS][ROW]; // (dt, dt u) of the way up, for the way down
     Place<R> at;
     const bool some = at.set(a, p, BWD_WAVES);
     const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE, row = at.row, j = at.j;
@@ -720,15 +752,14 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
                 fetch_up(b0 + (part + 1) * TS);
             else
                 fetch_down(b0 + (part + 1) * TS);
-            wave_sync();
 #pragma unroll
             for (int q = 0; q < Q; ++q)
-                *(float2 *)&s_step[wave][4 * q + row][j] = make_float2(dt[q], x[q]);
+                s_up[wave][part][4 * q + row][j] = make_float2(dt[q], x[q]);
             wave_sync();
             float2 v[TS];
 #pragma unroll
             for (int k = 0; k < TS; ++k)
-                v[k] = *(const float2 *)&s_step[wave][k][j];
+                v[k] = s_up[wave][part][k][j];
             each<TS>([&](auto tt) {
                 constexpr int step = tt;
                 each<R>([&](auto ii) {
@@ -752,7 +783,10 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
                 const bool counts = ru.inside(q, left) && at.real;
                 u[q] = counts ? (float)far_u[q] : 0.f;
                 raw[q] = (float)far_delta[q] + bias;
-                dt[q] = counts ? step_of(far_delta[q], bias, a.softplus) : 0.f;
+                if (part + 1 < parts)
+                    dt[q] = s_up[wave][part][4 * q + row][j].x;
+                else
+                    dt[q] = counts ? step_of(far_delta[q], bias, a.softplus) : 0.f;
                 dy[q] = counts ? (float)far_adj[q] : 0.f;
                 slope[q] = 0.f;
                 if constexpr (GATED) {
@@ -921,6 +955,7 @@ __global__ void __launch_bounds__(256) k_scan_mixed_sums(ScanArgs a, Plan p, con
     const float *x = sums + ((z * p.across + (int64_t)g * p.per_group) * a.len + t) * (2 * wide) + which * wide + n;
     const int64_t step = a.len * 2 * wide;
     float s = 0.f;
+#pragma unroll 8 // (loads together: 4 x 2048 x 4096 30 -> 12 us)
     for (int k = 0; k < p.per_group; ++k)
         s += x[k * step];
     const SeqRows &r = which ? a.adj_C : a.adj_B;
@@ -969,13 +1004,16 @@ Plan plan_of(const ScanArgs &a, bool adjoint)
     const int64_t per = a.dim / a.groups, wave_count = (per + ROW - 1) / ROW;
     p.per_group = (int)((wave_count + waves - 1) / waves);
     p.across = (int64_t)p.per_group * a.groups;
-    // A first walk costs a step of the forward about as much again, and half as much of the
-    // adjoint, which also needs two waves a SIMD more: 4 x 2048 x 4096 bf16 (1024 waves, one a
+    // A first walk costs a step of the forward about as much again, and less of the adjoint,
+    // which also needs two waves a SIMD more: 4 x 2048 x 4096 bf16 (1024 waves, one a
     // SIMD) forward 178 us whole, 219 in 4 segments, adjoint 900 and 721; 2 x 2048 x 4096 forward
-    // 160 in 2 segments, 126 in 8, adjoint 576 and 368.  More than 64 cost more to put
-    // together than they save (16384 x 256 forward 68 us, with 256 116).
+    // 160 in 2 segments, 126 in 8, adjoint 576 and 368.  Beyond 16 states a SIMD holds one wave
+    // of the adjoint, and segments only fill it (4 x 2048 x 4096 of 32 states 1601 us whole,
+    // 1790 in 4).  More than 64 segments cost more to put together than they save (16384 x 256
+    // forward 68 us, with 256 116).
     const int64_t all = a.batch * a.groups * wave_count, blocks = std::max<int64_t>(1, (a.len + block - 1) / block);
-    const int64_t want = all >= (adjoint ? 1536 : 768) ? 1 : std::min<int64_t>({blocks, 64, 4096 / all});
+    const bool two = !adjoint || a.states <= 16;
+    const int64_t want = all >= (adjoint && two ? 1536 : 768) ? 1 : std::min<int64_t>({blocks, 64, (two ? 4096 : 1024) / all});
     const int64_t each = (blocks + want - 1) / want;
     p.segment = (int)std::min<int64_t>(each * block, INT32_MAX);
     p.segments = (int)((blocks + each - 1) / each);
