@@ -9,6 +9,7 @@ of its tensors.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 from typing import NamedTuple, Optional
 
@@ -71,6 +72,7 @@ def _conv_sizes(x, w):
     return (*x.shape, w.shape[1])
 
 
+@functools.lru_cache(maxsize=1024)
 def chol_causal_conv_adjoint_workspace_size(dtype_code: int, batch: int, length: int, dim: int, width: int) -> int:
     out = ctypes.c_size_t(0)
     _check(lib.chol_causal_conv_adjoint_workspace_size(dtype_code, batch, length, dim, width, ctypes.byref(out)))
@@ -134,12 +136,14 @@ _ARGS = struct.Struct("@5q2i" + 6 * "Pqq" + "6P" + 6 * "Pqq" + "5P")
 _NO_ROWS = (0, 0, 0)
 
 
+@functools.lru_cache(maxsize=1024)
 def chol_selective_scan_workspace_size(adjoint: bool, batch: int, length: int, dim: int, groups: int, states: int) -> int:
     out = ctypes.c_size_t(0)
     _check(lib.chol_selective_scan_workspace_size(int(adjoint), batch, length, dim, groups, states, ctypes.byref(out)))
     return int(out.value)
 
 
+@functools.lru_cache(maxsize=1024)
 def chol_selective_scan_block(states: int) -> int:
     """Steps between two of the states that a forward call saves."""
     block = int(lib.chol_selective_scan_block(states))
@@ -289,6 +293,7 @@ def _logits(x, tokens):
     return x.shape
 
 
+@functools.lru_cache(maxsize=1024)
 def chol_token_logprob_workspace_size(dtype_code: int, rows: int, vocab: int, top: int) -> int:
     out = ctypes.c_size_t(0)
     _check(lib.chol_token_logprob_workspace_size(dtype_code, rows, vocab, top, ctypes.byref(out)))
