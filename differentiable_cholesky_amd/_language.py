@@ -16,7 +16,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from ._lib import _check, lib
-from ._train import _code, _on, _ptr, _raw_stream, _rows, _same, _scratch, _seq, _state
+from ._train import _code, _on, _ptr, _raw_stream, _rows, _same, _scratch, _seq
 
 CONV_WIDTHS = (2, 3, 4)
 SCAN_MAX_STATES = 64
@@ -46,20 +46,35 @@ _bind()
 def _like(t, name, like, shape=None, dtype=None):
     """t, checked, or a new tensor of that shape (default like's) and type (default like's)."""
     if t is None:
-        return torch.empty(like.shape if shape is None else shape, dtype=like.dtype if dtype is None else dtype,
-                           device=like.device)
+        return torch.empty_like(like) if shape is None else like.new_empty(shape, dtype=dtype)
     _same(t, name, like, shape, dtype)
     return t
 
 
 def _whole(t, name, like, shape, dtype=None):
-    """Pointer of a contiguous tensor of that shape and type (default like's), or None."""
+    """Pointer of a contiguous tensor of that shape and type (default like's); 0 for None."""
     if t is None:
-        return None
+        return 0
+    if dtype is None:
+        dtype = like.dtype
+    if t.dtype is dtype and t.shape == shape and t.get_device() == like.get_device() and t.is_contiguous():
+        return t.data_ptr()
     _same(t, name, like, shape, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _f32(t, name, like, shape):
+    return _whole(t, name, like, shape, torch.float32)
+
+
+def _steps(t, name, like):
+    """(pointer, ld, stride) of a [batch, len, dim] array of like's shape and type."""
+    if t is like or (t.dtype is like.dtype and t.shape == like.shape and t.get_device() == like.get_device()):
+        return _seq(t, name)
+    _same(t, name, like)
+    return _seq(t, name)
 
 
 # ------------------------------------------------------------- convolution ----
@@ -90,11 +105,12 @@ def chol_causal_conv(x, w, bias=None, state=None, last=None, y=None, silu: bool 
     pw, pb = _whole(w, "w", x, (dim, width)), _whole(bias, "bias", x, (dim,))
     kept = (batch, width - 1, dim)
     with _on(x, stream):
-        y = _like(y, "y", x)
+        if y is None:
+            y = torch.empty_like(x)
         if last is None:
-            last = torch.empty(kept, dtype=x.dtype, device=x.device)
-        _check(lib.chol_causal_conv(code, int(silu), batch, length, dim, width, *_seq(x, "x"), pw, pb,
-                                    _whole(state, "state", x, kept), _whole(last, "last", x, kept), *_seq(y, "y"),
+            last = x.new_empty(kept)
+        _check(lib.chol_causal_conv(code, silu, batch, length, dim, width, *_seq(x, "x"), pw, pb,
+                                    _whole(state, "state", x, kept), _whole(last, "last", x, kept), *_steps(y, "y", x),
                                     _raw_stream(x)))
     return y, last
 
@@ -122,9 +138,9 @@ def chol_causal_conv_adjoint(x, w, adj, bias=None, state=None, adjLast=None, sil
         keep, ws, wbytes = _scratch(chol_causal_conv_adjoint_workspace_size(code, batch, length, dim, width), x.device,
                                     workspace)
         _check(lib.chol_causal_conv_adjoint(
-            code, int(silu), batch, length, dim, width, *_seq(x, "x"), pw, pb, _whole(state, "state", x, kept),
+            code, silu, batch, length, dim, width, *_seq(x, "x"), pw, pb, _whole(state, "state", x, kept),
             *_seq(adj, "adj"), _whole(adjLast, "adjLast", x, kept), *_seq(adjX, "adjX"),
-            _state(adjW, "adjW", x, (dim, width)), _state(adjBias, "adjBias", x, (dim,)), int(accumulate),
+            _f32(adjW, "adjW", x, (dim, width)), _f32(adjBias, "adjBias", x, (dim,)), accumulate,
             _whole(adjState, "adjState", x, kept), ws, wbytes, _raw_stream(x)))
     return adjX, adjW, adjBias, adjState
 
@@ -134,6 +150,7 @@ def chol_causal_conv_adjoint(x, w, adj, bias=None, state=None, adjLast=None, sil
 # chol_scan_args: sizes, flags, six arrays, A D bias h0 hlast starts, six arrays, adj_hlast, adj_A adj_D adj_bias adj_h0
 _ARGS = struct.Struct("@5q2i" + 6 * "Pqq" + "6P" + 6 * "Pqq" + "5P")
 _NO_ROWS = (0, 0, 0)
+_NO_ADJOINT = (0,) * 23
 
 
 @functools.lru_cache(maxsize=1024)
@@ -173,18 +190,19 @@ def _scan_sizes(u, delta, A, B, C):
     if u.dim() != 3:
         raise ValueError("u must be [batch, len, dim]")
     batch, length, dim = u.shape
-    _same(delta, "delta", u)
     if A.dim() != 2 or A.shape[0] != dim:
         raise ValueError(f"A must be [dim, states], got {tuple(A.shape)}")
     states = A.shape[1]
     if not 1 <= states <= SCAN_MAX_STATES:
         raise ValueError(f"A must have 1 to {SCAN_MAX_STATES} states, got {states}")
-    if B.dim() not in (3, 4) or B.shape[-1] != states:
-        raise ValueError(f"B must be [batch, len, states] or [batch, len, groups, states], got {tuple(B.shape)}")
-    groups = B.shape[2] if B.dim() == 4 else 1
-    if groups < 1 or dim % groups:
-        raise ValueError(f"{groups} groups do not divide {dim} channels")
-    _same(B, "B", u, (batch, length, groups, states) if B.dim() == 4 else (batch, length, states))
+    if B.dim() == 4:
+        groups = B.shape[2]
+        if groups < 1 or dim % groups:
+            raise ValueError(f"{groups} groups do not divide {dim} channels")
+        _same(B, "B", u, (batch, length, groups, states))
+    else:
+        groups = 1
+        _same(B, "B", u, (batch, length, states))
     _same(C, "C", B)
     return batch, length, dim, groups, states
 
@@ -203,22 +221,19 @@ def chol_selective_scan(u, delta, A, B, C, D=None, z=None, bias=None, h0=None, h
     code = _code(u)
     batch, length, dim, groups, states = _scan_sizes(u, delta, A, B, C)
     with _on(u, stream):
-        y = _like(y, "y", u)
+        if y is None:
+            y = torch.empty_like(u)
         shape = (batch, dim, states)
         if hlast is None:
-            hlast = torch.empty(shape, dtype=torch.float32, device=u.device)
+            hlast = u.new_empty(shape, dtype=torch.float32)
         if save or starts is not None:
             starts = _like(starts, "starts", u, (batch, -(-length // chol_selective_scan_block(states)), dim, states),
                            torch.float32)
-        if z is not None:
-            _same(z, "z", u)
         args = _ARGS.pack(
-            batch, length, dim, groups, states, softplus, 0, *_seq(u, "u"), *_seq(delta, "delta"), *_mixed(B, "B"),
-            *_mixed(C, "C"), *(_NO_ROWS if z is None else _seq(z, "z")), *_seq(y, "y"),
-            _state(A, "A", u, (dim, states)), _state(D, "D", u, (dim,)) or 0, _state(bias, "bias", u, (dim,)) or 0,
-            _state(h0, "h0", u, shape) or 0, _state(hlast, "hlast", u, shape),
-            _whole(starts, "starts", u, None if starts is None else starts.shape, torch.float32) or 0,
-            *_NO_ROWS * 6, 0, 0, 0, 0, 0)
+            batch, length, dim, groups, states, softplus, 0, *_seq(u, "u"), *_steps(delta, "delta", u), *_mixed(B, "B"),
+            *_mixed(C, "C"), *(_NO_ROWS if z is None else _steps(z, "z", u)), *_steps(y, "y", u),
+            _f32(A, "A", u, (dim, states)), _f32(D, "D", u, (dim,)), _f32(bias, "bias", u, (dim,)), _f32(h0, "h0", u, shape),
+            _f32(hlast, "hlast", u, shape), 0 if starts is None else _f32(starts, "starts", u, starts.shape), *_NO_ADJOINT)
         need = chol_selective_scan_workspace_size(False, batch, length, dim, groups, states) if length > 1 else 0
         keep, ws, wbytes = _scratch(need, u.device, workspace)
         _check(lib.chol_selective_scan(code, args, ws, wbytes, _raw_stream(u)))
@@ -237,14 +252,15 @@ def chol_selective_scan_adjoint(u, delta, A, B, C, starts, adj, D=None, z=None, 
     ``adjHlast``.  adjA, adjD and adjBias are fp32 and added to with ``accumulate``."""
     code = _code(u)
     batch, length, dim, groups, states = _scan_sizes(u, delta, A, B, C)
-    _same(adj, "adj", u)
     blocks = -(-length // chol_selective_scan_block(states))
     with _on(u, stream):
-        adjU, adjDelta = _like(adjU, "adjU", u), _like(adjDelta, "adjDelta", u)
+        if adjU is None:
+            adjU = torch.empty_like(u)
+        if adjDelta is None:
+            adjDelta = torch.empty_like(u)
         adjB, adjC = _like(adjB, "adjB", B), _like(adjC, "adjC", C)
         if z is not None:
-            _same(z, "z", u)
-            adjZ = _like(adjZ, "adjZ", u)
+            adjZ = torch.empty_like(u) if adjZ is None else adjZ
         elif adjZ is not None:
             raise ValueError("adjZ needs z")
         new = u.new_zeros if accumulate else u.new_empty
@@ -256,16 +272,16 @@ def chol_selective_scan_adjoint(u, delta, A, B, C, starts, adj, D=None, z=None, 
             adjBias = new((dim,), dtype=torch.float32)
         shape = (batch, dim, states)
         if adjH0 is None:
-            adjH0 = torch.empty(shape, dtype=torch.float32, device=u.device)
+            adjH0 = u.new_empty(shape, dtype=torch.float32)
         args = _ARGS.pack(
-            batch, length, dim, groups, states, softplus, accumulate, *_seq(u, "u"), *_seq(delta, "delta"),
-            *_mixed(B, "B"), *_mixed(C, "C"), *(_NO_ROWS if z is None else _seq(z, "z")), *_NO_ROWS,
-            _state(A, "A", u, (dim, states)), _state(D, "D", u, (dim,)) or 0, _state(bias, "bias", u, (dim,)) or 0, 0, 0,
-            _whole(starts, "starts", u, (batch, blocks, dim, states), torch.float32), *_seq(adj, "adj"),
-            *_seq(adjU, "adjU"), *_seq(adjDelta, "adjDelta"), *_mixed(adjB, "adjB"), *_mixed(adjC, "adjC"),
-            *(_NO_ROWS if z is None else _seq(adjZ, "adjZ")), _state(adjHlast, "adjHlast", u, shape) or 0,
-            _state(adjA, "adjA", u, (dim, states)), _state(adjD, "adjD", u, (dim,)) or 0,
-            _state(adjBias, "adjBias", u, (dim,)) or 0, _state(adjH0, "adjH0", u, shape))
+            batch, length, dim, groups, states, softplus, accumulate, *_seq(u, "u"), *_steps(delta, "delta", u),
+            *_mixed(B, "B"), *_mixed(C, "C"), *(_NO_ROWS if z is None else _steps(z, "z", u)), *_NO_ROWS,
+            _f32(A, "A", u, (dim, states)), _f32(D, "D", u, (dim,)), _f32(bias, "bias", u, (dim,)), 0, 0,
+            _f32(starts, "starts", u, (batch, blocks, dim, states)), *_steps(adj, "adj", u), *_steps(adjU, "adjU", u),
+            *_steps(adjDelta, "adjDelta", u), *_mixed(adjB, "adjB"), *_mixed(adjC, "adjC"),
+            *(_NO_ROWS if z is None else _steps(adjZ, "adjZ", u)), _f32(adjHlast, "adjHlast", u, shape),
+            _f32(adjA, "adjA", u, (dim, states)), _f32(adjD, "adjD", u, (dim,)), _f32(adjBias, "adjBias", u, (dim,)),
+            _f32(adjH0, "adjH0", u, shape))
         need = chol_selective_scan_workspace_size(True, batch, length, dim, groups, states)
         keep, ws, wbytes = _scratch(need, u.device, workspace)
         _check(lib.chol_selective_scan_adjoint(code, args, ws, wbytes, _raw_stream(u)))
@@ -311,12 +327,13 @@ def chol_token_logprob(logits, tokens, scale: float = 1.0, top: int = 0, entropy
         raise ValueError(f"top must be 0 to {min(vocab, LOGPROB_MAX_TOP)}, got {top}")
     with _on(logits, stream):
         px, ldx = _rows(logits, "logits")
-        f32, dev = torch.float32, logits.device
-        logp, lse = torch.empty(rows, dtype=f32, device=dev), torch.empty(rows, dtype=f32, device=dev)
-        h = torch.empty(rows, dtype=f32, device=dev) if entropy else None
-        ids = torch.empty((rows, top), dtype=torch.int64, device=dev) if top else None
-        top_logp = torch.empty((rows, top), dtype=f32, device=dev) if top else None
-        keep, ws, wbytes = _scratch(chol_token_logprob_workspace_size(code, rows, vocab, top), dev, workspace)
+        logp, lse, *h = logits.new_empty((3 if entropy else 2, rows), dtype=torch.float32).unbind(0)
+        h = h[0] if entropy else None
+        ids = top_logp = None
+        if top:
+            ids = logits.new_empty((rows, top), dtype=torch.int64)
+            top_logp = logits.new_empty((rows, top), dtype=torch.float32)
+        keep, ws, wbytes = _scratch(chol_token_logprob_workspace_size(code, rows, vocab, top), logits.device, workspace)
         _check(lib.chol_token_logprob(code, rows, vocab, px, ldx, tokens.data_ptr(), scale, logp.data_ptr(),
                                       lse.data_ptr(), _ptr(h), top, _ptr(top_logp), _ptr(ids), ws, wbytes,
                                       _raw_stream(logits)))
@@ -338,7 +355,7 @@ def chol_token_logprob_adjoint(logits, tokens, lse, adjLogp=None, entropy=None, 
         px, ldx = _rows(logits, "logits")
         pa, lda = _rows(adjLogits, "adjLogits")
         _check(lib.chol_token_logprob_adjoint(
-            code, rows, vocab, px, ldx, tokens.data_ptr(), scale, _state(lse, "lse", logits, (rows,)),
-            _state(entropy, "entropy", logits, (rows,)), _state(adjLogp, "adjLogp", logits, (rows,)),
-            _state(adjEntropy, "adjEntropy", logits, (rows,)), pa, lda, _raw_stream(logits)))
+            code, rows, vocab, px, ldx, tokens.data_ptr(), scale, _f32(lse, "lse", logits, (rows,)),
+            _f32(entropy, "entropy", logits, (rows,)), _f32(adjLogp, "adjLogp", logits, (rows,)),
+            _f32(adjEntropy, "adjEntropy", logits, (rows,)), pa, lda, _raw_stream(logits)))
     return adjLogits
