@@ -250,11 +250,22 @@ chol_status chol_causal_conv_adjoint(chol_dtype dt, int silu, int64_t batch, int
 
 namespace {
 
+// The kernels count steps in 32 bits, and reach 16 rows on by offsets of 32 bits in bytes.
+const int64_t MAX_LEN = (int64_t)1 << 30, MAX_ROW = (int64_t)1 << 25;
+
+template <int N> bool rows_near(const Array (&arrays)[N])
+{
+    for (const Array &a : arrays)
+        if (!a.empty() && a.rows > 1 && a.ld > MAX_ROW)
+            return false;
+    return true;
+}
+
 chol_status scan_sizes(int64_t batch, int64_t len, int64_t dim, int64_t groups, int64_t states)
 {
     if (batch < 0 || len < 0 || dim < 0 || groups < 1 || states < 1 || dim % groups != 0)
         return CHOL_ERR_INVALID_VALUE;
-    if (states > CHOL_SCAN_MAX_STATES || batch > INT32_MAX || len > INT32_MAX || dim > INT32_MAX ||
+    if (states > CHOL_SCAN_MAX_STATES || batch > INT32_MAX || len > MAX_LEN || dim > INT32_MAX ||
         (__int128)batch * dim * states > INT32_MAX)
         return CHOL_ERR_NOT_SUPPORTED;
     return CHOL_OK;
@@ -332,6 +343,8 @@ chol_status chol_selective_scan(chol_dtype dt, const chol_scan_args *args, void 
     const chol_status r = arrays_ok(in, out, may, workspace, need);
     if (r != CHOL_OK)
         return r;
+    if (!rows_near(in) || !rows_near(out))
+        return CHOL_ERR_NOT_SUPPORTED;
     const chol_status q = workspace_ok(workspace, workspace_bytes, need, 4);
     if (q != CHOL_OK)
         return q;
@@ -375,6 +388,8 @@ chol_status chol_selective_scan_adjoint(chol_dtype dt, const chol_scan_args *arg
     const chol_status r = arrays_ok(in, out, may, workspace, need);
     if (r != CHOL_OK)
         return r;
+    if (!rows_near(in) || !rows_near(out))
+        return CHOL_ERR_NOT_SUPPORTED;
     const chol_status q = workspace_ok(workspace, workspace_bytes, need, 4);
     if (q != CHOL_OK)
         return q;

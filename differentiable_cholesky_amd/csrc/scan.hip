@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
     __shared__ vec<float, 4> s_step[BWD_WAVES][TS][ROW];
     __shared__ vec<float, 4> s_B[BWD_WAVES][TS][R], s_C[BWD_WAVES][TS][R];
     __shared__ float s_sum[2][BWD_WAVES][2][REGS][WAVE];
-    __shared__ vec<float, 4> s_state[BWD_WAVES][PARTS - 1][R / 4][WAVE];
+    __shared__ vec<float, 4> s_state[BWD_WAVES][PARTS - 2][R / 4][WAVE]; // (but for the first and the last)
     __shared__ float2 s_up[BWD_WAVES][PARTS - 1][TS][ROW]; // (dt, dt u) of the way up, for the way down
     Place<R> at;
     const bool some = at.set(a, p, BWD_WAVES);
@@ -702,6 +702,22 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
     sums += (at.z * p.across + blockIdx.x % (unsigned)p.across) * a.len * (8 * R);
     float dD = 0.f, dbias = 0.f;
     int turn = 0;
+    // The waves' sums of a part.  (The other half is written while this one is read: a wave
+    // reaches the next barrier only after it has read.)
+    const auto add_up = [&](int t) {
+#pragma unroll
+        for (int i = threadIdx.x; i < 2 * REGS * WAVE; i += BWD_WAVES * WAVE) {
+            const int which = i / (REGS * WAVE), reg = i / WAVE % REGS, l = i % WAVE;
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < BWD_WAVES; ++w)
+                s += s_sum[turn][w][which][reg][l];
+            const int step = t + reg * PER + l % ROW / R;
+            if (step < at.to)
+                sums[(int64_t)step * (8 * R) + which * 4 * R + R * (l / ROW) + l % R] = s;
+        }
+        turn ^= 1;
+    };
     // a part's inputs are on their way while the one before it is walked
     T far_u[Q], far_delta[Q], far_z[Q], far_adj[Q], far_B[REGS], far_C[REGS];
     float far_start[R];
@@ -725,14 +741,27 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
         rC.load(far_C, t, left);
     };
     const int last = at.from + (at.to - 1 - at.from) / BLOCK * BLOCK;
-    fetch_start(last);
-    at.to - last > TS ? fetch_up(last) : fetch_down(last);
+    if (!some) { // a wave without channels adds zeros, and its share of the sums over the waves
+#pragma unroll
+        for (int k = 0; k < 2 * 2 * REGS; ++k)
+            s_sum[k / (2 * REGS)][wave][k / REGS % 2][k % REGS][lane] = 0.f;
+    } else {
+        fetch_start(last);
+        at.to - last > TS ? fetch_up(last) : fetch_down(last);
+    }
     for (int b0 = last; b0 >= at.from; b0 -= BLOCK) {
         float start[R];
 #pragma unroll
         for (int i = 0; i < R; ++i)
             start[i] = at.real ? far_start[i] : 0.f;
         const int parts = (min(at.to - b0, BLOCK) + TS - 1) / TS;
+        if (!some) {
+            for (int part = parts - 1; part >= 0; --part) {
+                __syncthreads();
+                add_up(b0 + part * TS);
+            }
+            continue;
+        }
         // the states that the parts start from
         float h0[R];
 #pragma unroll
@@ -768,11 +797,12 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
                                  v[step].y * of_row<step % PER * R + i>(B[step / PER]));
                 });
             });
+            if (part + 2 < parts)
 #pragma unroll
-            for (int k = 0; k < R / 4; ++k) {
-                const vec<float, 4> w = {h0[4 * k], h0[4 * k + 1], h0[4 * k + 2], h0[4 * k + 3]};
-                s_state[wave][part][k][lane] = w;
-            }
+                for (int k = 0; k < R / 4; ++k) {
+                    const vec<float, 4> w = {h0[4 * k], h0[4 * k + 1], h0[4 * k + 2], h0[4 * k + 3]};
+                    s_state[wave][part][k][lane] = w;
+                }
         }
         // (the last part starts where that walk ended: h0)
         for (int part = parts - 1; part >= 0; --part) {
@@ -809,7 +839,11 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
             float first[R];
 #pragma unroll
             for (int i = 0; i < R; ++i)
-                first[i] = part == 0 ? start[i] : part == parts - 1 ? h0[i] : s_state[wave][part - 1][i / 4][lane][i % 4];
+                first[i] = part == 0 ? start[i] : h0[i];
+            if (part > 0 && part < parts - 1)
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    first[i] = s_state[wave][part - 1][i / 4][lane][i % 4];
             wave_sync();
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
@@ -913,21 +947,8 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
                             wz.store(t, q, out_z[q]);
                     }
             }
-            // (the other half is written while this one is read: a wave reaches the next
-            // barrier only after it has read)
             __syncthreads();
-#pragma unroll
-            for (int i = threadIdx.x; i < 2 * REGS * WAVE; i += BWD_WAVES * WAVE) {
-                const int which = i / (REGS * WAVE), reg = i / WAVE % REGS, l = i % WAVE;
-                float s = 0.f;
-#pragma unroll
-                for (int w = 0; w < BWD_WAVES; ++w)
-                    s += s_sum[turn][w][which][reg][l];
-                const int step = t + reg * PER + l % ROW / R;
-                if (step < at.to)
-                    sums[(int64_t)step * (8 * R) + which * 4 * R + R * (l / ROW) + l % R] = s;
-            }
-            turn ^= 1;
+            add_up(t);
         }
     }
     dD = over_rows(dD), dbias = over_rows(dbias);
@@ -1007,12 +1028,12 @@ Plan plan_of(const ScanArgs &a, bool adjoint)
     // A first walk costs a step of the forward about as much again, and less of the adjoint,
     // which also needs two waves a SIMD more: 4 x 2048 x 4096 bf16 (1024 waves, one a
     // SIMD) forward 178 us whole, 219 in 4 segments, adjoint 900 and 721; 2 x 2048 x 4096 forward
-    // 160 in 2 segments, 126 in 8, adjoint 576 and 368.  Beyond 16 states a SIMD holds one wave
-    // of the adjoint, and segments only fill it (4 x 2048 x 4096 of 32 states 1601 us whole,
-    // 1790 in 4).  More than 64 segments cost more to put together than they save (16384 x 256
+    // 160 in 2 segments, 126 in 8, adjoint 576 and 368.  Beyond 32 states a SIMD holds one wave
+    // of the adjoint, and segments only fill it (4 x 2048 x 4096 of 64 states 2790 us whole,
+    // 3100 in 4).  More than 64 segments cost more to put together than they save (16384 x 256
     // forward 68 us, with 256 116).
     const int64_t all = a.batch * a.groups * wave_count, blocks = std::max<int64_t>(1, (a.len + block - 1) / block);
-    const bool two = !adjoint || a.states <= 16;
+    const bool two = !adjoint || a.states <= 32;
     const int64_t want = all >= (adjoint && two ? 1536 : 768) ? 1 : std::min<int64_t>({blocks, 64, (two ? 4096 : 1024) / all});
     const int64_t each = (blocks + want - 1) / want;
     p.segment = (int)std::min<int64_t>(each * block, INT32_MAX);

@@ -750,9 +750,10 @@ typedef struct {
  * chol_selective_scan, chol_selective_scan_adjoint -- the scan of chol_scan_args,
  * and its adjoint.  workspace: at least as many bytes as the _workspace_size
  * call gives (4-byte aligned; NULL allowed when it is 0).
- * states above CHOL_SCAN_MAX_STATES, batch * dim * states above 2^31 - 1, and
- * sizes that need 2^32 threads or more, return CHOL_ERR_NOT_SUPPORTED; groups that
- * do not divide dim return CHOL_ERR_INVALID_VALUE.
+ * states above CHOL_SCAN_MAX_STATES, len above 2^30, batch * dim * states above
+ * 2^31 - 1, rows of one sequence more than 2^25 elements apart, and sizes that need
+ * 2^32 threads or more, return CHOL_ERR_NOT_SUPPORTED; groups that do not divide dim
+ * return CHOL_ERR_INVALID_VALUE.
  */
 chol_status chol_selective_scan(chol_dtype dtype, const chol_scan_args *args, void *workspace, size_t workspace_bytes,
                                 void *stream);

@@ -98,7 +98,9 @@ def scan_adjoint(dt=BF16, ws=P[25], wbytes=1 << 40, **change):
 @pytest.mark.parametrize("change,expect", [
     (dict(dt=F64), INVALID), (dict(batch=-1), INVALID), (dict(length=-1), INVALID), (dict(dim=-2), INVALID), (dict(groups=0), INVALID),
     (dict(groups=3), INVALID), (dict(states=0), INVALID), (dict(states=65), NOTSUP), (dict(batch=0), OK), (dict(dim=0), OK),
-    (dict(batch=1 << 20, dim=1 << 10), NOTSUP), (dict(length=1 << 31), NOTSUP),
+    (dict(batch=1 << 20, dim=1 << 10), NOTSUP), (dict(length=(1 << 30) + 1), NOTSUP),
+    (dict(batch=1, length=2, u=(P[0], (1 << 25) + 1, 0)), NOTSUP), (dict(batch=1, length=2, y=(P[5], 1 << 26, 0)), NOTSUP),
+    (dict(batch=1, length=2, C=(P[3], 1 << 30, 0)), NOTSUP), (dict(batch=1, B=(P[2], 1 << 41, 0)), INVALID),
     (dict(u=(0, *ROWS)), INVALID), (dict(delta=(0, *ROWS)), INVALID), (dict(B=(0, *MIXED)), INVALID), (dict(C=(0, *MIXED)), INVALID),
     (dict(y=(0, *ROWS)), INVALID), (dict(A=0), INVALID), (dict(hlast=0), INVALID),
     (dict(u=(P[0], 63, 6400)), INVALID), (dict(B=(P[2], 31, 3200)), INVALID), (dict(C=(P[3], 32, 3199)), INVALID),
@@ -113,6 +115,7 @@ def test_scan_refusals(change, expect):
 
 
 @pytest.mark.parametrize("change,expect", [
+    (dict(batch=1, length=2, adj_z=(P[17], 1 << 26, 0)), NOTSUP), (dict(batch=1, length=2, adj=(P[12], 1 << 26, 0)), NOTSUP),
     (dict(dt=F64), INVALID), (dict(states=65), NOTSUP), (dict(dim=0), OK), (dict(starts=0), INVALID), (dict(adj=(0, *ROWS)), INVALID),
     (dict(adj_u=(0, *ROWS)), INVALID), (dict(adj_z=(0, *ROWS)), INVALID), (dict(adj_B=(0, *MIXED)), INVALID), (dict(adj_A=0), INVALID),
     (dict(adj_A=P[19] + 1), INVALID), (dict(adj_delta=(P[0], *ROWS)), INVALID), (dict(adj_u=(P[4], *ROWS)), INVALID),
