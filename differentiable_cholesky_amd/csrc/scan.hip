@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(FWD_WAVES *WAVE) k_scan_adjoint_ends(ScanArgs 
     for (int t = last; t >= at.from; t -= STEPS, half ^= 1) {
         wave_sync();
         // the steps' operands are read a group ahead of their use
-        constexpr int AHEAD = R > 8 ? 2 : 4;
+        constexpr int AHEAD = R > 8 ? 2 : R > 4 ? 4 : 8;
         struct {
             float2 v[AHEAD];
             vec<float, 4> c[AHEAD][R / 4];
@@ -962,50 +962,53 @@ __global__ void __launch_bounds__(BWD_WAVES *WAVE, R < 16 ? 2 : 1)
         o[a.states] = dD, o[a.states + 1] = dbias;
 }
 
-// adj_B and adj_C: over a group's workgroups.  A thread a (step, group, state) of one.
-template <typename T>
-__global__ void __launch_bounds__(256) k_scan_mixed_sums(ScanArgs a, Plan p, const float *sums, int wide)
-{
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, count = a.batch * a.len * a.groups * 2 * a.states;
-    if (i >= count)
-        return;
-    const int n = (int)(i % a.states), which = (int)(i / a.states % 2);
-    const int64_t rest = i / a.states / 2, t = rest % a.len;
-    const int g = (int)(rest / a.len % a.groups);
-    const int64_t z = rest / a.len / a.groups;
-    const float *x = sums + ((z * p.across + (int64_t)g * p.per_group) * a.len + t) * (2 * wide) + which * wide + n;
-    const int64_t step = a.len * 2 * wide;
-    float s = 0.f;
-#pragma unroll 8 // (loads together: 4 x 2048 x 4096 30 -> 12 us)
-    for (int k = 0; k < p.per_group; ++k)
-        s += x[k * step];
-    const SeqRows &r = which ? a.adj_C : a.adj_B;
-    ((T *)r.p)[z * r.stride + t * r.ld + (int64_t)g * a.states + n] = (T)s;
-}
+// The first `mixed` workgroups: adj_B and adj_C, over a group's workgroups, a thread a
+// (step, group, state) of one.  The others: adj_A, adj_D and adj_bias, over batch and
+// segments, a column a lane, sixteen waves' sums of every sixteenth row joined.
+constexpr int SUM_THREADS = 1024, SUM_WAVES = SUM_THREADS / WAVE;
 
-// adj_A, adj_D and adj_bias: over batch and segments.
-__global__ void __launch_bounds__(1024) k_scan_own_sums(ScanArgs a, const float *own, int64_t rows)
+template <typename T>
+__global__ void __launch_bounds__(SUM_THREADS) k_scan_sums(ScanArgs a, Plan p, const float *sums, int wide, unsigned mixed,
+                                                           const float *own)
 {
-    __shared__ float s_sum[16][WAVE];
-    const int lane = threadIdx.x % WAVE, slot = threadIdx.x / WAVE;
-    const int64_t i = (int64_t)blockIdx.x * WAVE + lane, cols = a.dim * (a.states + 2);
+    __shared__ float s_sum[SUM_WAVES][WAVE];
     float s = 0.f;
+    if (blockIdx.x < mixed) {
+        const int64_t i = (int64_t)blockIdx.x * SUM_THREADS + threadIdx.x, count = a.batch * a.len * a.groups * 2 * a.states;
+        if (i >= count)
+            return;
+        const int n = (int)(i % a.states), which = (int)(i / a.states % 2);
+        const int64_t rest = i / a.states / 2, t = rest % a.len;
+        const int g = (int)(rest / a.len % a.groups);
+        const int64_t z = rest / a.len / a.groups;
+        const float *x = sums + ((z * p.across + (int64_t)g * p.per_group) * a.len + t) * (2 * wide) + which * wide + n;
+        const int64_t step = a.len * 2 * wide;
+#pragma unroll 8 // (loads together: 4 x 2048 x 4096 30 -> 12 us)
+        for (int k = 0; k < p.per_group; ++k)
+            s += x[k * step];
+        const SeqRows &r = which ? a.adj_C : a.adj_B;
+        ((T *)r.p)[z * r.stride + t * r.ld + (int64_t)g * a.states + n] = (T)s;
+        return;
+    }
+    const int lane = threadIdx.x % WAVE, slot = threadIdx.x / WAVE;
+    const int64_t i = (int64_t)(blockIdx.x - mixed) * WAVE + lane, cols = a.dim * (a.states + 2), rows = a.batch * p.segments;
     if (i < cols)
-        for (int64_t r = slot; r < rows; r += 16)
+        for (int64_t r = slot; r < rows; r += SUM_WAVES)
             s += own[r * cols + i];
     s_sum[slot][lane] = s;
     __syncthreads();
     if (slot > 0 || i >= cols)
         return;
 #pragma unroll
-    for (int k = 1; k < 16; ++k)
+    for (int k = 1; k < SUM_WAVES; ++k)
         s += s_sum[k][lane];
     const int64_t c = i / (a.states + 2);
     const int n = (int)(i % (a.states + 2));
-    float *out = n < a.states ? a.adj_A + c * a.states + n : n == a.states ? a.adj_D + (a.adj_D ? c : 0) : a.adj_bias + (a.adj_bias ? c : 0);
-    if (n >= a.states && !(n == a.states ? a.adj_D : a.adj_bias))
-        return;
-    *out = a.accumulate ? *out + s : s;
+    float *out = n < a.states    ? a.adj_A + c * a.states + n
+                 : n == a.states ? (a.adj_D ? a.adj_D + c : nullptr)
+                                 : (a.adj_bias ? a.adj_bias + c : nullptr);
+    if (out)
+        *out = a.accumulate ? *out + s : s;
 }
 
 // An empty sequence's states and gradients: the given ones, or zero.
@@ -1098,7 +1101,7 @@ int64_t scan_adjoint_workspace(const ScanArgs &a)
 {
     const Plan p = plan_of(a, true);
     if (!grid_ok((double)a.batch * p.across * p.segments * BWD_WAVES * WAVE) ||
-        !grid_ok((double)a.batch * a.len * a.groups * 2 * a.states + 256) ||
+        !grid_ok((double)a.batch * a.len * a.groups * 2 * a.states + (double)a.dim * (a.states + 2) * SUM_WAVES + 4096) ||
         !grid_ok((double)a.batch * a.dim * a.states + 256))
         return -1;
     return a.len > 0 ? (maps_size(a, p) + sums_size(a, p) + own_size(a, p)) * (int64_t)sizeof(float) : 0;
@@ -1171,11 +1174,10 @@ chol_status scan_adjoint(chol_dtype dt, const ScanArgs &a, void *ws, hipStream_t
             };
             a.z.p ? launch(k_scan_adjoint<T, R, true>) : launch(k_scan_adjoint<T, R, false>);
             CHOL_LAUNCH_CHECK();
-            hipLaunchKernelGGL((k_scan_mixed_sums<T>), dim3((unsigned)ceil_of(a.batch * a.len * a.groups * 2 * a.states, 256)),
-                               dim3(256), 0, st, a, p, (const float *)sums, 4 * R);
-            CHOL_LAUNCH_CHECK();
-            hipLaunchKernelGGL(k_scan_own_sums, dim3((unsigned)ceil_of(a.dim * (a.states + 2), WAVE)), dim3(1024), 0, st, a,
-                               (const float *)own, a.batch * p.segments);
+            const unsigned mixed = (unsigned)ceil_of(a.batch * a.len * a.groups * 2 * a.states, SUM_THREADS);
+            const unsigned rest = (unsigned)ceil_of(a.dim * (a.states + 2), WAVE);
+            hipLaunchKernelGGL((k_scan_sums<T>), dim3(mixed + rest), dim3(SUM_THREADS), 0, st, a, p, (const float *)sums, 4 * R,
+                               mixed, (const float *)own);
             CHOL_LAUNCH_CHECK();
             return CHOL_OK;
         });
