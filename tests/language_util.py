@@ -83,9 +83,9 @@ def conv_adjoint(x, w, adj, bias, state, adj_last, silu):
     if adj_last is not None:
         d[:, length:] += adj_last.double()
         de[:, length:] += (k + 2) * U * adj_last.double().abs()
-    # a run of at most 72 steps, the runs of a workgroup, every sixteenth workgroup, sixteen sums
+    # a run of at most 128 steps, the runs of a workgroup, every sixteenth workgroup, sixteen sums
     n = x.shape[0] * length
-    depth = min(n, 72 + 256 + n // 128 + 16) + 1
+    depth = min(n, 128 + 256 + n // 128 + 16) + 1
     dw = torch.stack([(q * rows[:, i:i + length]).sum((0, 1)) for i in range(k)], 1)
     dwe = torch.stack([((qe + depth * U * q.abs()) * rows[:, i:i + length].abs()).sum((0, 1)) for i in range(k)], 1)
     db, dbe = q.sum((0, 1)), (qe + depth * U * q.abs()).sum((0, 1))
