@@ -509,11 +509,11 @@ template <typename T, int S>
 __global__ void __launch_bounds__(256) k_scan_step(ScanArgs a)
 {
     constexpr bool FULL = sizeof(T) == 4;
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / S;
-    if (at >= a.batch * a.dim)
+    const unsigned one = (blockIdx.x * 256 + threadIdx.x) / S, dim = (unsigned)a.dim; // (the states are fewer than 2^31)
+    if (one >= (unsigned)a.batch * dim)
         return;
-    const int64_t z = at / a.dim;
-    const int c = (int)(at % a.dim), g = c / (int)(a.dim / a.groups), n0 = (threadIdx.x % S) * 4;
+    const int64_t at = one, z = one / dim;
+    const int c = (int)(one % dim), g = a.groups == 1 ? 0 : c / (int)(dim / (unsigned)a.groups), n0 = (threadIdx.x % S) * 4;
     const int64_t left = a.states - n0;
     const vec<float, 4> A = load_some<float, 4>(a.A + (int64_t)c * a.states + n0, left);
     vec<float, 4> h = {0.f, 0.f, 0.f, 0.f};
