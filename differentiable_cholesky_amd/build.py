@@ -19,7 +19,7 @@ OUT = os.path.join(HERE, "libchol.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["small.hip", "blocked.hip", "api.cpp", "profile.cpp", "side.cpp", "plan.cpp", "stream.hip", "solve.hip", "upper.hip", "complex.hip",
            "recurrence.hip", "rmsnorm.hip", "adamw.hip", "train.cpp",
-           "conv.hip", "scan.hip", "logprob.hip", "language.cpp"]
+           "conv.hip", "scan.hip", "scan_adjoint.hip", "logprob.hip", "language.cpp"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = [
