@@ -54,14 +54,14 @@ __device__ __forceinline__ float over_rows(float x)
 }
 // log(1 + exp(x)): the larger of x and 0, and log(1 + w) with w = exp(-|x|).  Where
 // u = 1 + w is rounded, what it lost is added (the logarithm's slope there is 1 / u; w
-// is small where it matters).  The hardware's logarithm is within 1.2e-7 on all of (1, 2).
+// is small where it matters).  NaN stays one by the choice (a maximum would drop it).  The hardware's logarithm is within 1.2e-7 on all of (1, 2).
 __device__ __forceinline__ float softplus_of(float x)
 {
     // exp(-|x|) with its product's low part (expf_of); at -110, where it is 0, and below
     const float v = fmaxf(-fabsf(x), -110.f), y = v * LOG2E, e = __builtin_amdgcn_exp2f(y);
     const float low = fmaf(v, (float)(1.4426950408889634074 - LOG2E), fmaf(v, LOG2E, -y));
     const float w = fmaf(e * LN2, low, e), u = 1.f + w;
-    return fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(u), LN2, w - (u - 1.f));
+    return (x < 0.f ? 0.f : x) + fmaf(__builtin_amdgcn_logf(u), LN2, w - (u - 1.f));
 }
 
 struct Plan {

@@ -194,6 +194,30 @@ def test_non_finite_inputs_stay_in_their_channel(length):
         assert torch.equal(got[k][:, :, 0], grads[k][:, :, 0]), k
 
 
+@pytest.mark.parametrize("softplus", [True, False])
+@pytest.mark.parametrize("length", [1, 90, 900])
+@pytest.mark.parametrize("key", ["delta", "B", "C", "z"])
+def test_nan_of_any_input_reaches_the_results(key, length, softplus):
+    """A step's NaN is in its results, and from there on in the state (but for C and z)."""
+    s = make(1, length, 40, 1, 16, torch.float32, seed=3)
+    if not softplus:
+        s["delta"], s["bias"] = torch.exp(s["delta"]), s["bias"].abs()
+    y, last, _ = forward(s, softplus=softplus)
+    at = length // 2
+    s[key][0, at, ..., 3] = float("nan")
+    y2, last2, _ = forward(s, softplus=softplus)
+    kept = key in ("C", "z")
+    channels = torch.arange(40, device="cuda") == 3 if key in ("delta", "z") else torch.ones(40, dtype=torch.bool, device="cuda")
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[0, at:at + 1 if kept else length, channels] = True
+    assert torch.equal(torch.isnan(y2), bad) and torch.equal(y2[~bad], y[~bad])
+    if kept:
+        assert torch.equal(last2, last)
+    else:
+        states = torch.arange(16, device="cuda") == 3 if key == "B" else torch.ones(16, dtype=torch.bool, device="cuda")
+        assert torch.equal(torch.isnan(last2[0]), channels[:, None] & states)
+
+
 def test_closed_and_open_steps():
     """Steps so long that the state is forgotten, and of zero, which leave it as it is."""
     s = make(1, 60, 20, 1, 16, torch.float32, full=False, seed=5)
