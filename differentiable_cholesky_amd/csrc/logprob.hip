@@ -81,6 +81,9 @@ struct Stats {
     float m, s, t;
 };
 
+// t, relative to a maximum d above (d < 0; e = 2^(d k), where it is 0 d may be anything).
+__device__ __forceinline__ float shifted(const Stats &st, float d, float e) { return e == 0.f ? 0.f : fmaf(d, st.s, st.t) * e; }
+
 __device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stats st, const void *x, float given)
 {
     const float log_s = __builtin_amdgcn_logf(st.s) * LN2;
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
         for (int v = 0; v < V; ++v) {
             const float d = (float)x[i][v] - ref, e = __builtin_amdgcn_exp2f(d * k2);
             s += e;
-            w = fmaf(fmaxf(d, -1e30f), e, w); // (e is 0 at -inf)
+            w = fmaf(fmaxf(d, -__FLT_MAX__), e, w); // (e is 0 at -inf)
         }
     const float lane_sum = s;
     s = wave_sum(s), w = wave_sum(w);
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
             if (o.m > -INFINITY || o.s != o.s) {
                 const float d = o.m - all.m, e = __builtin_amdgcn_exp2f(d * k2);
                 all.s = fmaf(o.s, e, all.s);
-                all.t = fmaf(fmaf(d, o.s, o.t), e, all.t);
+                all.t += shifted(o, d, e);
             }
         }
     } else {
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(WAVE) k_logprob_join(LogprobArgs a, int chunks
     if (st.m > -INFINITY || st.s != st.s) {
         const float d = st.m - all.m, e = __builtin_amdgcn_exp2f(d * k2);
         s = st.s * e;
-        t = fmaf(d, st.s, st.t) * e;
+        t = shifted(st, d, e);
     }
     all.s = wave_sum(s), all.t = wave_sum(t);
     if (lane == 0)
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob_adjoint(LogprobAdjArgs a, u
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const float lp = fmaf(a.scale, (float)in[i][v], -lse), p = __builtin_amdgcn_exp2f(lp * LOG2E);
-            float g = -p * fmaf(ge, fmaxf(lp, -1e30f) + H, gl); // (p is 0 at -inf)
+            float g = -p * fmaf(ge, fmaxf(lp, -200.f) + H, gl); // (p is 0 from there on down)
             if (c + v == token)
                 g += gl;
             out[v] = (T)(empty ? 0.f : a.scale * g);

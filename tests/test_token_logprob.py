@@ -96,6 +96,30 @@ def test_closed_columns_and_rows(vocab, dtype):
     tu.near(d[keep], ref, bound, "closed adjoint")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,vocab", [(2, 40), (3, 5000), (2, 33000), (600, 33000)])
+def test_one_open_column(rows, vocab, dtype):
+    """All but one column at the type's lowest value, so that waves and chunks hold nothing else."""
+    x, tokens, gl, ge = make(rows, vocab, dtype, seed=vocab)
+    row = torch.arange(rows, device="cuda")
+    column = row * 7919 % vocab
+    open_ = x[row, column]
+    x.fill_(torch.finfo(dtype).min)
+    x[row, column] = open_
+    tokens[::2] = column[::2]
+    check(x, tokens, gl, ge, 1.0, 0, "one open")
+
+
+@pytest.mark.parametrize("rows,vocab", [(2, 900), (2, 40000)])
+def test_small_scales_of_large_logits(rows, vocab):
+    x, tokens, gl, ge = make(rows, vocab, torch.float32, seed=9)
+    import differentiable_cholesky_amd as dc
+    x, scale = x * 2.0 ** 117, 2.0 ** -117
+    got, want = dc.chol_token_logprob(x, tokens, scale=scale), dc.chol_token_logprob(x * scale, tokens)
+    for a, b in zip(got[:3], want[:3]):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("vocab", [60, 5000, 40000])
 def test_non_finite_rows_stay_alone(vocab):
     import differentiable_cholesky_amd as dc
