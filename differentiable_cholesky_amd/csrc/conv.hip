@@ -367,7 +367,8 @@ bool conv_fits(chol_dtype dt, const ConvArgs &a)
 int64_t conv_adjoint_workspace(chol_dtype dt, const ConvArgs &a)
 {
     const Plan p = dt == CHOL_F32 ? adjoint_plan<float>(a) : adjoint_plan<bf16_t>(a);
-    return grid_ok(a, p) ? a.batch * p.along * a.dim * (a.width + 1) * (int64_t)sizeof(float) : -1;
+    // (and the threads of the sums)
+    return grid_ok(a, p) && (double)(a.dim * (a.width + 1) + WAVE) * 16 <= 4294967295.0 ? a.batch * p.along * a.dim * (a.width + 1) * (int64_t)sizeof(float) : -1;
 }
 
 chol_status conv(chol_dtype dt, const ConvArgs &a, hipStream_t st)

@@ -192,7 +192,7 @@ chol_status chol_causal_conv_adjoint_workspace_size(chol_dtype dt, int64_t batch
         return CHOL_ERR_INVALID_VALUE;
     *bytes = 0;
     const chol_status s = conv_sizes(dt, batch, len, dim, width);
-    if (s != CHOL_OK || batch == 0 || dim == 0)
+    if (s != CHOL_OK || dim == 0)
         return s;
     ConvArgs a{};
     a.batch = batch, a.len = len, a.dim = dim, a.width = (int)width;
@@ -266,7 +266,7 @@ chol_status scan_sizes(int64_t batch, int64_t len, int64_t dim, int64_t groups, 
     if (batch < 0 || len < 0 || dim < 0 || groups < 1 || states < 1 || dim % groups != 0)
         return CHOL_ERR_INVALID_VALUE;
     if (states > CHOL_SCAN_MAX_STATES || batch > INT32_MAX || len > MAX_LEN || dim > INT32_MAX ||
-        (__int128)batch * dim * states > INT32_MAX)
+        (__int128)std::max<int64_t>(batch, 1) * dim * states > INT32_MAX)
         return CHOL_ERR_NOT_SUPPORTED;
     return CHOL_OK;
 }

@@ -133,6 +133,17 @@ def test_scan_no_arguments():
     assert lib.chol_selective_scan_adjoint(BF16, None, None, 0, None) == INVALID
 
 
+def test_launches_that_a_call_of_no_elements_makes_still_fit():
+    """Without a batch the gradients of the weights are written all the same, a thread or more each."""
+    out = ctypes.c_size_t(1)
+    conv, scan_ = lib.chol_causal_conv_adjoint_workspace_size, lib.chol_selective_scan_workspace_size
+    for batch in (0, 1):
+        assert conv(BF16, batch, 1, 1 << 25, 4, ctypes.byref(out)) == OK
+        assert conv(BF16, batch, 1, 1 << 28, 4, ctypes.byref(out)) == NOTSUP
+        assert scan_(1, batch, 0, 1 << 20, 1, 16, ctypes.byref(out)) == OK
+        assert scan_(1, batch, 0, 1 << 28, 1, 16, ctypes.byref(out)) == NOTSUP
+
+
 def test_scan_sizes():
     block = lib.chol_selective_scan_block
     assert [block(n) for n in (-1, 0, 1, 16, 17, 32, 33, 64, 65)] == [-1, -1, 64, 64, 32, 32, 16, 16, -1]
