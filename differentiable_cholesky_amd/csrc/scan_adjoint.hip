@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(WAVES *WAVE) k_scan_adjoint_ends(ScanArgs a, P
     __shared__ float2 s_step[2][WAVES][STEPS][ROW];
     __shared__ vec<float, 4> s_C[2][WAVES][STEPS][R];
     Place<R> at;
-    if (!at.set(a, p, WAVES))
+    if (!at.set(a, p, p.waves))
         return;
     const int wave = threadIdx.x / WAVE, row = at.row, j = at.j;
     float A2[R], mu[R];
@@ -560,7 +560,7 @@ chol_status scan_adjoint(chol_dtype dt, const ScanArgs &a, void *ws, hipStream_t
             float *maps = (float *)ws, *sums = maps + maps_size(a, p), *own = sums + sums_size(a, p);
             if (p.segments > 1) {
                 hipLaunchKernelGGL((k_scan_adjoint_ends<T, R>), dim3((unsigned)(a.batch * p.across * p.segments)),
-                                   dim3(WAVES * WAVE), 0, st, a, p, maps);
+                                   dim3(p.waves * WAVE), 0, st, a, p, maps);
                 CHOL_LAUNCH_CHECK();
             }
             const auto launch = [&](auto kernel) {
@@ -569,6 +569,8 @@ chol_status scan_adjoint(chol_dtype dt, const ScanArgs &a, void *ws, hipStream_t
             };
             if (p.waves == 1)
                 a.z.p ? launch(k_scan_adjoint<T, R, true, 1>) : launch(k_scan_adjoint<T, R, false, 1>);
+            else if (p.waves == 2)
+                a.z.p ? launch(k_scan_adjoint<T, R, true, 2>) : launch(k_scan_adjoint<T, R, false, 2>);
             else
                 a.z.p ? launch(k_scan_adjoint<T, R, true, WAVES>) : launch(k_scan_adjoint<T, R, false, WAVES>);
             CHOL_LAUNCH_CHECK();
