@@ -5,18 +5,22 @@
 //   entropy = log s - sum (y - m) e^(y - m) / s
 //   adj_x_j = scale (gl (1[j = token] - p_j) - ge p_j (log p_j + entropy)),  p = e^(y - lse)
 //
-// Memory bounds both: forward reads a row once, the adjoint reads and writes it once.  A
+// Memory bounds both: forward reads a row once, the adjoint reads and writes it once
+// (4096 x 128000 bf16 173 us, 6.1 TB/s, and 398 us, 5.3 TB/s).  A
 // row is cut into chunks that stay in the registers of a wave (short rows, four to a
 // workgroup) or of a workgroup, so that the maximum, the sums relative to it and the
 // search for alternatives take one reading.  Several chunks a row (long rows, or few of
 // them) are joined by a second launch, one wave a row.
 //
-// Alternatives: a wave's k-th largest maximum of a lane is a bound that k elements reach,
-// so only lanes that reach it, hardly more than k, can hold one.  Their elements go through
-// LDS, a lane an element; those that reach the bound are ranked one after the other
-// (4096 x 128000 bf16, 8 alternatives 288 us; comparing every element in its own lane took
-// 896).  Where lanes or elements are too many (equal values, sorted rows) the wave finds each
-// alternative in turn among its registers, k times the comparisons.  Order: by value, then by
+// Alternatives: the k-th largest maximum of a lane is a bound that k elements reach, so only
+// lanes that reach it, hardly more than k of the workgroup, can hold one.  Their elements go
+// through LDS, a lane an element; those that reach the bound are ranked against each other
+// (4096 x 128000 bf16 with 1, 8 and 20 alternatives 191, 244 and 293 us, where the search's own
+// vector instructions and barriers add to a kernel that fills three quarters of the units; a
+// bound and a list for each wave, found by comparing all lanes, took 221, 291 and 415, and
+// comparing every element in its own lane 896 for 8).  Where lanes or elements are too many
+// (equal values, sorted rows) a wave finds each
+// alternative in turn among its elements, k times the comparisons.  Order: by value, then by
 // the lower index; NaN before all.
 #include <algorithm>
 #include <climits>
@@ -61,6 +65,42 @@ __device__ __forceinline__ int wave_max(int x)
 __device__ __forceinline__ int wave_min(int x)
 {
     return over_wave(x, [](int a, int b) { return min(a, b); });
+}
+
+// How many of `lanes` are before this one.
+__device__ __forceinline__ int before_lane(uint64_t lanes)
+{
+    return __builtin_amdgcn_mbcnt_hi((unsigned)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)lanes, 0));
+}
+
+// A key that `top` or more of the wave's keys reach (all are above NONE and `most` is the
+// greatest) and, unless several are equal, exactly so many: first by steps down from the
+// greatest, each eight times the last, then by halving.  A comparison a turn, the rest is scalar.
+template <int N> __device__ __forceinline__ int reached_by(const int (&keys)[N], int most, int top)
+{
+    const auto reach = [&](int key) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            n += __popcll(__ballot(keys[i] >= key));
+        return n;
+    };
+    int high = most, low = most, n = top > 1 ? reach(most) : 1;
+    if (n >= top)
+        return most;
+    for (unsigned step = 1u << 20; n < top; step *= 8) {
+        high = low;
+        low = step != 0 && (unsigned)most - (unsigned)NONE > step ? most - (int)step : NONE;
+        n = reach(low);
+    }
+    while (n != top && (unsigned)high - (unsigned)low > 1) {
+        const int half = (int)((unsigned)low + ((unsigned)high - (unsigned)low) / 2), r = reach(half);
+        if (r < top)
+            high = half;
+        else
+            low = half, n = r;
+    }
+    return low;
 }
 
 struct Entry {
@@ -113,7 +153,8 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
     __shared__ Entry s_some[TOP ? WAVES : 1][WAVE], s_list[TOP ? WAVES : 1][MOST];
     __shared__ vec<T, V> s_lane[TOP ? WAVES : 1][SLOTS][NV];
     __shared__ int s_column[TOP ? WAVES : 1][SLOTS];
-    __shared__ alignas(16) float s_max[TOP ? WAVES : 1][WAVE];
+    __shared__ float s_max[TOP ? WAVES : 1][WAVE], s_bound;
+    __shared__ int s_count;
     const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE, t = threadIdx.x % LANES;
     const int64_t unit = (int64_t)blockIdx.x * (WAVES / TEAM) + (TEAM == 1 ? wave : 0);
     if (unit >= a.rows * chunks) // (waves of their own where TEAM is 1)
@@ -155,27 +196,41 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
     const float lane_sum = s;
     s = wave_sum(s), w = wave_sum(w);
     const Stats mine{m, s, w};
+    if constexpr (TEAM > 1)
+        if (lane == 0)
+            s_stats[wave] = mine;
 
+    int count = 0; // elements that may be alternatives, of the workgroup (TEAM 1: of the wave)
+    const int list = TEAM > 1 ? 0 : wave;
     if constexpr (TOP) {
         const int top = a.top;
-        // lanes with fewer than k maxima above their own hold the k-th largest or more
-        s_max[wave][lane] = lane_max;
-        wave_sync();
-        int above = 0;
+        // k of the lanes' maxima, so k elements, reach the bound
+        float bound;
+        if constexpr (TEAM == 1) {
+            const int keys[1] = {key_of(lane_max)};
+            bound = value_of(reached_by(keys, __builtin_amdgcn_readfirstlane(key_of(m)), top));
+        } else {
+            s_max[wave][lane] = lane_max;
+            if (threadIdx.x == 0)
+                s_count = 0;
+            __syncthreads();
+            if (wave == 0) {
+                int keys[TEAM];
+                float most = m;
 #pragma unroll
-        for (int l = 0; l < WAVE; l += 4) {
-            const vec<float, 4> other = *(const vec<float, 4> *)&s_max[wave][l];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                above += other[k] > lane_max ? 1 : 0;
+                for (int i = 0; i < TEAM; ++i) {
+                    keys[i] = key_of(s_max[i][lane]);
+                    most = fmaxf(most, s_stats[i].m);
+                }
+                s_bound = value_of(reached_by(keys, __builtin_amdgcn_readfirstlane(key_of(most)), top));
+            }
+            __syncthreads();
+            bound = s_bound;
         }
-        const float bound = -wave_max(above < top ? -lane_max : -INFINITY);
         // (a NaN makes its lane's sum one)
-        const bool holds = above < top || lane_sum != lane_sum;
+        const bool holds = lane_max >= bound || lane_sum != lane_sum;
         const uint64_t holders = __ballot(holds);
-        const int slots = __popcll(holders);
-        const int slot = __builtin_amdgcn_mbcnt_hi((unsigned)(holders >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)holders, 0));
-        int count = 0;
+        const int slots = __popcll(holders), slot = before_lane(holders);
         if (slots <= SLOTS) {
             if (holds) {
 #pragma unroll
@@ -188,27 +243,43 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
                 const int from = at / N, k = at % N, c = from < slots ? s_column[wave][from] + k / V * (LANES * V) + k % V : end;
                 const float y = from < slots ? (float)s_lane[wave][from][k / V][k % V] : -INFINITY;
                 const uint64_t who = __ballot(!(y < bound) && c < end);
-                const int place = count + __builtin_amdgcn_mbcnt_hi((unsigned)(who >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)who, 0));
+                int first = count;
+                if constexpr (TEAM > 1) { // (in any order: places in the list are by value and index)
+                    if (who && lane == 0)
+                        first = atomicAdd(&s_count, __popcll(who));
+                    first = __builtin_amdgcn_readfirstlane(first);
+                }
+                const int place = first + before_lane(who);
                 if ((who >> lane & 1) && place < WAVE)
-                    s_some[wave][place] = {key_of(y), c};
-                count += __popcll(who);
+                    s_some[list][place] = {key_of(y), c};
+                if constexpr (TEAM == 1)
+                    count += __popcll(who);
             }
-        } else {
+        } else if (TEAM == 1) {
             count = WAVE + 1;
+        } else if (lane == 0) {
+            atomicAdd(&s_count, WAVE + 1);
         }
-        wave_sync();
+        if constexpr (TEAM > 1) {
+            __syncthreads();
+            count = s_count;
+            if (count <= WAVE && wave > 0)
+                return;
+        } else {
+            wave_sync();
+        }
         if (count <= WAVE) {
             // a lane's place is the number of those before it
             Entry e{NONE, INT_MAX};
             if (lane < count)
-                e = s_some[wave][lane];
+                e = s_some[list][lane];
             int before = 0;
             for (int l = 0; l < count; ++l)
-                before += e.after(s_some[wave][l]) ? 1 : 0;
+                before += e.after(s_some[list][l]) ? 1 : 0;
             if (lane < top)
-                s_list[wave][lane] = {NONE, INT_MAX};
+                s_list[list][lane] = {NONE, INT_MAX};
             if (lane < count && before < top)
-                s_list[wave][before] = e;
+                s_list[list][before] = e;
         } else {
             // (from memory again: from registers it would be as many instructions as elements)
             Entry last{INT_MAX, -1};
@@ -230,11 +301,11 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
 
     Stats all = mine;
     if constexpr (TEAM > 1) {
-        if (lane == 0)
-            s_stats[wave] = mine;
-        __syncthreads();
-        if (wave > 0)
-            return;
+        if (!TOP || count > WAVE) { // (else the waves have met, and only the first is here)
+            __syncthreads();
+            if (wave > 0)
+                return;
+        }
 #pragma unroll
         for (int i = 0; i < TEAM; ++i)
             all.m = fmaxf(all.m, s_stats[i].m);
@@ -248,9 +319,9 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
                 all.t += shifted(o, d, e);
             }
         }
-    } else {
-        wave_sync();
     }
+    if constexpr (TOP)
+        wave_sync();
     if (lane == 0) {
         if (chunks > 1)
             stats[unit] = all;
@@ -259,12 +330,12 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
     }
     if constexpr (TOP) {
         const float lse = all.m == -INFINITY ? -INFINITY : fmaf(a.scale, all.m, __builtin_amdgcn_logf(all.s) * LN2);
-        // The waves' lists together: an entry's place is its own and, in each other list, the
+        // The waves' lists (where there are any) together: an entry's place is its own and, in each other list, the
         // number of those before it (found by halving; entries that are none come last)
         Entry mine{NONE, INT_MAX};
-        if constexpr (TEAM == 1) {
+        if (TEAM == 1 || count <= WAVE) {
             if (lane < a.top)
-                mine = s_list[wave][lane];
+                mine = s_list[list][lane];
         } else {
             if (lane < a.top)
                 s_some[0][lane] = mine;
