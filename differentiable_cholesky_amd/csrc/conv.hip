@@ -6,7 +6,8 @@
 //   q_t = adj_t silu'(p_t),  adj_x_t = sum_k w_k q_{t+K-1-k} (+ adj_last),
 //   adj_w_k = sum q_t x_{t-K+1+k},  adj_bias = sum q_t
 //
-// A few operations an element, so memory bounds it.  A thread walks `run` steps of V
+// A few operations an element, so memory bounds it (8 x 4096 x 4096 bf16 105 us, 5.1 TB/s,
+// adjoint 172, 4.7; 64 x 1 x 4096 4.4 on the GPU).  A thread walks `run` steps of V
 // channels and keeps the last K - 1 rows in registers, so a row is read once, and
 // K - 1 more a run (the adjoint: two rows K - 1 times).  Lanes lie along the channels
 // as far as these reach and along runs from there on, so that neighbouring runs, which
