@@ -46,6 +46,40 @@ template <typename T, typename F> __device__ __forceinline__ T over_wave(T x, F 
     return f(h.a, h.b);
 }
 
+// Lane j of a row gets the sum over the row's lanes of x[j].  Halves of the row, then of
+// those, exchange what they do not keep: x[k] + its exchange goes to all lanes, and that of
+// x[k + 8] (k + 4) over the upper half (the bank mask names groups of four lanes whose
+// result is written).  Written with selections the compiler takes 47 instructions, this 35.
+// An operand of an exchange has to be two instructions old: s_nop 1 sees to it for what
+// comes in, and the order below has it for the rest.  Results are written before the last
+// operand is read: none may share its register, not even where both hold one value ("&").
+__device__ __forceinline__ float over_lanes(const float (&in)[16], int lane)
+{
+    float x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+        x[k] = in[k];
+#define EXCHANGE(k, from, ctrl, mask) "v_add_f32_dpp %" #k ", %" #from ", %" #from " " ctrl " row_mask:0xf bank_mask:" mask "\n\t"
+#define BOTH(k, far, ctrl, mask) EXCHANGE(k, k, ctrl, "0xf") EXCHANGE(k, far, ctrl, mask)
+#define FAR(k, far) BOTH(k, far, "row_ror:8", "0xc")         // lanes l and l + 8
+#define MID(k, far) BOTH(k, far, "row_half_mirror", "0xa")   // l and l ^ 7
+    asm("s_nop 1\n\t"
+        FAR(0, 8) FAR(1, 9) FAR(2, 10) FAR(3, 11) FAR(4, 12) FAR(5, 13) FAR(6, 14) FAR(7, 15)
+        MID(0, 4) MID(1, 5) MID(2, 6) MID(3, 7)
+        EXCHANGE(0, 0, "quad_perm:[2,3,0,1]", "0xf") EXCHANGE(1, 1, "quad_perm:[2,3,0,1]", "0xf")
+        EXCHANGE(2, 2, "quad_perm:[2,3,0,1]", "0xf") EXCHANGE(3, 3, "quad_perm:[2,3,0,1]", "0xf")
+        EXCHANGE(0, 0, "quad_perm:[1,0,3,2]", "0xf") EXCHANGE(1, 1, "quad_perm:[1,0,3,2]", "0xf")
+        EXCHANGE(2, 2, "quad_perm:[1,0,3,2]", "0xf") EXCHANGE(3, 3, "quad_perm:[1,0,3,2]", "0xf")
+        : "+&v"(x[0]), "+&v"(x[1]), "+&v"(x[2]), "+&v"(x[3]), "+&v"(x[4]), "+&v"(x[5]), "+&v"(x[6]), "+&v"(x[7])
+        : "v"(x[8]), "v"(x[9]), "v"(x[10]), "v"(x[11]), "v"(x[12]), "v"(x[13]), "v"(x[14]), "v"(x[15]));
+#undef MID
+#undef FAR
+#undef BOTH
+#undef EXCHANGE
+    const float lo = lane & 1 ? x[1] : x[0], hi = lane & 1 ? x[3] : x[2];
+    return lane & 2 ? hi : lo;
+}
+
 // LDS written by lanes of a wave and read by others of the same wave, whose operations
 // on it are in order.
 __device__ __forceinline__ void wave_sync()
