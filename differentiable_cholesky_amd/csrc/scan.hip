@@ -96,8 +96,9 @@ __global__ void __launch_bounds__(WAVES *WAVE, R > 4 ? 1 : 3) k_scan(ScanArgs a,
         }
 #pragma unroll
         for (int k = 0; k < REGS; ++k) {
-            next_B[k] = no_state ? 0.f : (float)far_B[k];
-            ((float *)&s_mixed[half][wave][k * PER + j / R][0])[R * row + j % R] = ENDS ? next_B[k] : no_state ? 0.f : (float)far_C[k];
+            const bool none = no_state || (!whole && !rB.inside(k, at.to - t)); // (0 times a B of inf would be NaN)
+            next_B[k] = none ? 0.f : (float)far_B[k];
+            ((float *)&s_mixed[half][wave][k * PER + j / R][0])[R * row + j % R] = ENDS ? next_B[k] : none ? 0.f : (float)far_C[k];
         }
     };
     float *start = nullptr;

@@ -64,11 +64,12 @@ __global__ void __launch_bounds__(WAVES *WAVE) k_scan_adjoint_ends(ScanArgs a, P
         rz.template load<W>(far_z, t, at.to - t);
         rC.template load<W>(far_C, t, at.to - t);
     };
-    // what arrived, into LDS; steps past the end leave mu as it is
-    const auto stage = [&](int t, int half) {
+    // what arrived, into LDS; steps past the end (none in a `whole` block) leave mu as it is: their C too
+    // is 0, for 0 times an infinite one would be NaN
+    const auto stage = [&](int t, int half, auto whole) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const bool counts = rdelta.inside(q, at.to - t);
+            const bool counts = whole || rdelta.inside(q, at.to - t);
             const float gate = (float)far_z[q], sg = sigmoid_of<FULL>(gate);
             const float dy = (float)far_adj[q] * (gated ? gate * sg : 1.f);
             const float dt = counts ? step_of(far_delta[q], bias, a.softplus) : 0.f;
@@ -77,12 +78,13 @@ __global__ void __launch_bounds__(WAVES *WAVE) k_scan_adjoint_ends(ScanArgs a, P
         }
 #pragma unroll
         for (int k = 0; k < REGS; ++k)
-            ((float *)&s_C[half][wave][k * PER + j / R][0])[R * row + j % R] = no_state ? 0.f : (float)far_C[k];
+            ((float *)&s_C[half][wave][k * PER + j / R][0])[R * row + j % R] =
+                no_state || (!whole && !rC.inside(k, at.to - t)) ? 0.f : (float)far_C[k];
     };
     int half = 0;
     const int last = at.from + (at.to - 1 - at.from) / STEPS * STEPS;
     fetch(last, std::false_type());
-    stage(last, 0);
+    stage(last, 0, std::false_type());
     if (last > at.from)
         fetch(last - STEPS, std::true_type());
     for (int t = last; t >= at.from; t -= STEPS, half ^= 1) {
@@ -104,7 +106,7 @@ __global__ void __launch_bounds__(WAVES *WAVE) k_scan_adjoint_ends(ScanArgs a, P
         };
         read(STEPS - 1);
         if (t > at.from) {
-            stage(t - STEPS, half ^ 1);
+            stage(t - STEPS, half ^ 1, std::true_type());
             if (t - STEPS > at.from)
                 fetch(t - 2 * STEPS, std::true_type());
         }
@@ -307,8 +309,10 @@ __global__ void __launch_bounds__(W *WAVE, R < 16 ? 2 : 1)
             }
 #pragma unroll
             for (int k = 0; k < REGS; ++k) {
-                B[k] = no_state ? 0.f : (float)far_B[k];
-                C[k] = no_state ? 0.f : (float)far_C[k];
+                // (steps past the end too: 0 times an infinite B or C would be NaN)
+                const bool none = no_state || !rB.inside(k, left);
+                B[k] = none ? 0.f : (float)far_B[k];
+                C[k] = none ? 0.f : (float)far_C[k];
             }
             if (part > 0) {
                 fetch_down(t - TS);
