@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(WAVES *WAVE, R > 4 ? 1 : 3) k_scan(ScanArgs a,
     load_states<R>(a.A + (int64_t)at.c * a.states, at.n0, a.states, A2);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        A2[i] *= LOG2E;
+        A2[i] = base2_rate(A2[i]);
         h[i] = 0.f;
     }
     const float bias = a.bias ? a.bias[at.c] : 0.f, D = a.D ? a.D[at.c] : 0.f;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(256) k_scan_step(ScanArgs a)
     float y = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(__builtin_amdgcn_exp2f(dt * (A[i] * LOG2E)), h[i], x * (float)B[i]);
+        h[i] = fmaf(__builtin_amdgcn_exp2f(dt * base2_rate(A[i])), h[i], x * (float)B[i]);
         y = fmaf((float)C[i], h[i], y);
     }
     store_some<float, 4>(a.hlast + at * a.states + n0, left, h);

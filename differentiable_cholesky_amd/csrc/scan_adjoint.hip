@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(WAVES *WAVE) k_scan_adjoint_ends(ScanArgs a, P
     load_states<R>(a.A + (int64_t)at.c * a.states, at.n0, a.states, A2);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        A2[i] *= LOG2E;
+        A2[i] = base2_rate(A2[i]);
         mu[i] = 0.f;
     }
     const float bias = a.bias ? a.bias[at.c] : 0.f;
@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(W *WAVE, R < 16 ? 2 : 1)
     load_states<R>(a.A + (int64_t)at.c * a.states, at.n0, a.states, A);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        A2[i] = A[i] * LOG2E;
+        A2[i] = base2_rate(A[i]);
+        A[i] = finite_rate(A[i]);
         mu[i] = dA[i] = 0.f;
     }
     const float bias = a.bias ? a.bias[at.c] : 0.f, D = a.D ? a.D[at.c] : 0.f;

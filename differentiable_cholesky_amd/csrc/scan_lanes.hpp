@@ -200,6 +200,13 @@ template <int R> __device__ __forceinline__ void store_states(float *p, int n0, 
     }
 }
 
+// A of -inf, under which exp(dt A) is 0, as the lowest number, under which it is 0 for any dt above
+// 2^-120.  So it is 1 for dt = 0 (steps past the end, lanes without a channel), where 0 times -inf
+// would be NaN, and what A multiplies in the gradients is 0.  NaN stays one.
+__device__ __forceinline__ float finite_rate(float A) { return A < -__FLT_MAX__ ? -__FLT_MAX__ : A; }
+// log2(e) A, for a base of 2.
+__device__ __forceinline__ float base2_rate(float A) { return finite_rate(A * LOG2E); }
+
 // A segment's map, for the walk that composes them: Q of every state, the steps' sum.
 struct Maps {
     float *Q, *sum;

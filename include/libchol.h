@@ -733,7 +733,10 @@ typedef struct {
  * terms are added in an order that depends on the sizes only.  exp(dt A) is within
  * (3 |dt A| + 2) 2^-24 of itself.  A long run of steps is also composed as
  * exp(A sum dt): A of at most 0 is what that is meant for; where it overflows, the
- * result is inf or NaN.
+ * result is inf or NaN.  A of -inf counts as the lowest number: exp(dt A) is 0 for dt
+ * above 2^-120 and 1 for dt = 0, and A's share in adj_delta is 0 with it.  Where dt u or
+ * a state is infinite, y and the gradients of that channel are inf or NaN, and NaN may
+ * stand for an inf.
  */
 typedef struct {
     int64_t batch, len, dim, groups, states;

@@ -66,3 +66,34 @@ def test_an_infinite_entry_of_the_last_row(batch, length, dim, groups, states):
         assert torch.equal(got[k], clean[k]), k
     for k in ("u", "delta", "z", "C"):
         assert torch.equal(got[k][:, :-1], clean[k][:, :-1]) and torch.equal(got[k][1:], clean[k][1:]), k
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("batch,length,dim,groups,states", ODD)
+def test_states_that_forget_at_once(batch, length, dim, groups, states, dtype):
+    """A of -inf: exp(dt A) is 0 for any step, and what A multiplies in the gradients is 0 too."""
+    s = scan_inputs(batch, length, dim, groups, states, dtype, seed=length)
+    gone = torch.rand(dim, states, generator=torch.Generator().manual_seed(1)).cuda() < 0.3
+    gone[:, 0] = False
+    gone[-1, :] = True
+    # (the 64-bit form with steps so long that the exponential is 0: the smallest dt here is above 1e-4)
+    s["A"] = torch.where(gone, -1e8, s["A"])
+    ref = lu.Scan64(*(s[k] for k in KEYS))
+    s["A"] = torch.where(gone, -math.inf, s["A"])
+    y, last, starts = scan_forward(s, save=True)
+    (y64, l64), (yb, lb) = ref.forward()
+    tu.near(y, y64, yb, "y")
+    tu.near(last, l64, lb, "last")
+    got = scan_adjoint(s, starts)
+    out, bounds = ref.adjoint(s["adj"], s["adj_last"])
+    for k in KEYS:
+        tu.near(got[k].view(out[k].shape), out[k], bounds[k], f"adjoint {k}")
+    # the same a token at a time, and NaN stays one
+    kept, rows = s["h0"].clone(), []
+    for t in range(min(length, 40)):
+        part = {k: x[:, t:t + 1] if k in STEPWISE else x for k, x in s.items()}
+        rows.append(scan_forward(part, h0=kept, hlast=kept)[0])
+    tu.near(torch.cat(rows, 1), y64[:, :40], yb[:, :40], "stepped y")
+    s["A"][0, 0] = math.nan
+    y2, last2, _ = scan_forward(s)
+    assert torch.isnan(y2[:, :, 0]).all() and torch.isnan(last2[:, 0, 0]).all() and torch.equal(last2[:, 1:], last[:, 1:])
