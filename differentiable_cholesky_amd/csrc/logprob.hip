@@ -1,7 +1,7 @@
 // Log probabilities of given tokens, entropy and the most likely alternatives of rows of
 // logits, and the gradient that reaches the logits.
 //
-//   y = scale x,  m = max y,  s = sum e^(y - m),  lse = m + log s,  logp = y_token - lse
+//   y = scale x,  m = max y,  s = sum e^(y - m),  lse = m + log s,  logp = (y_token - m) - log s
 //   entropy = log s - sum (y - m) e^(y - m) / s
 //   adj_x_j = scale (gl (1[j = token] - p_j) - ge p_j (log p_j + entropy)),  p = e^(y - lse)
 //
@@ -124,15 +124,21 @@ struct Stats {
 // t, relative to a maximum d above (d < 0; e = 2^(d k), where it is 0 d may be anything).
 __device__ __forceinline__ float shifted(const Stats &st, float d, float e) { return e == 0.f ? 0.f : fmaf(d, st.s, st.t) * e; }
 
-__device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stats st, const void *x, float given)
+// Natural logarithm of the sum, and of a logit's probability.  The latter from the distance to the
+// maximum: from lse, whose rounding grows with the logits, a likely token's could come out above 0.
+__device__ __forceinline__ float log_sum(const Stats &st) { return __builtin_amdgcn_logf(st.s) * LN2; }
+__device__ __forceinline__ float log_prob(float scale, const Stats &st, float x)
 {
-    const float log_s = __builtin_amdgcn_logf(st.s) * LN2;
+    return x == -INFINITY && st.s == st.s ? x : fmaf(scale, x - st.m, -log_sum(st));
+}
+
+__device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stats st, float given)
+{
+    const float log_s = log_sum(st);
     const float lse = st.m == -INFINITY ? -INFINITY : fmaf(a.scale, st.m, log_s);
     a.lse[row] = st.s != st.s ? st.s : lse; // NaN
     const int64_t token = a.tokens[row];
-    a.logp[row] = token < 0 || token >= a.vocab  ? 0.f
-                  : given == -INFINITY && st.s == st.s ? -INFINITY
-                                                 : fmaf(a.scale, given, -a.lse[row]);
+    a.logp[row] = token < 0 || token >= a.vocab ? 0.f : log_prob(a.scale, st, given);
     if (a.entropy)
         a.entropy[row] = st.m == -INFINITY && st.s == st.s ? 0.f : log_s - a.scale * (st.t / st.s);
 }
@@ -326,10 +332,9 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
         if (chunks > 1)
             stats[unit] = all;
         else
-            finish(a, row, all, a.x, given_logit<T>(a, row));
+            finish(a, row, all, given_logit<T>(a, row));
     }
     if constexpr (TOP) {
-        const float lse = all.m == -INFINITY ? -INFINITY : fmaf(a.scale, all.m, __builtin_amdgcn_logf(all.s) * LN2);
         // The waves' lists (where there are any) together: an entry's place is its own and, in each other list, the
         // number of those before it (found by halving; entries that are none come last)
         Entry mine{NONE, INT_MAX};
@@ -368,9 +373,8 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
             if (chunks > 1) {
                 lists[unit * a.top + lane] = mine;
             } else {
-                const float x = value_of(mine.key);
                 a.top_ids[row * a.top + lane] = mine.index;
-                a.top_logp[row * a.top + lane] = x == -INFINITY && all.s == all.s ? x : fmaf(a.scale, x, -lse);
+                a.top_logp[row * a.top + lane] = log_prob(a.scale, all, value_of(mine.key));
             }
         }
     }
@@ -399,11 +403,10 @@ __global__ void __launch_bounds__(WAVE) k_logprob_join(LogprobArgs a, int chunks
     }
     all.s = wave_sum(s), all.t = wave_sum(t);
     if (lane == 0)
-        finish(a, row, all, a.x, given);
+        finish(a, row, all, given);
     if (a.top == 0)
         return;
     wave_sync();
-    const float lse = all.m == -INFINITY ? -INFINITY : fmaf(a.scale, all.m, __builtin_amdgcn_logf(all.s) * LN2);
     const Entry *list = s_lists + lane * a.top;
     int at = 0;
     Entry mine{NONE, INT_MAX}, e = lane < chunks ? list[0] : mine;
@@ -417,9 +420,8 @@ __global__ void __launch_bounds__(WAVE) k_logprob_join(LogprobArgs a, int chunks
             mine = f;
     }
     if (lane < a.top) {
-        const float x = value_of(mine.key);
         a.top_ids[row * a.top + lane] = mine.index;
-        a.top_logp[row * a.top + lane] = x == -INFINITY && all.s == all.s ? x : fmaf(a.scale, x, -lse);
+        a.top_logp[row * a.top + lane] = log_prob(a.scale, all, value_of(mine.key));
     }
 }
 

@@ -789,6 +789,8 @@ int64_t chol_selective_scan_block(int64_t states);
  *           top_ids [out] device int64 [rows, top], the columns of the largest
  *           logits, the lowest first among equal ones, and top_logp [out] device
  *           fp32 [rows, top].
+ * logp and top_logp are taken from the row's maximum, not from lse: they are at most 0
+ * and do not depend on an offset that all logits of a row share.
  * A logit of -inf has no probability.  A row of nothing else has lse and logp -inf
  * and entropy 0; a row that holds NaN or +inf has NaN, as its definition has (NaN is
  * the first of its alternatives).
@@ -812,6 +814,7 @@ chol_status chol_token_logprob_workspace_size(chol_dtype dtype, int64_t rows, in
  *     adjX_j = scale (adjLogp (1[j = token] - p_j) - adjEntropy p_j (log p_j + entropy)).
  *   x, tokens, scale  [in] as the forward call had them; lse, entropy [in] what it
  *           wrote (entropy may be NULL where adjEntropy is).
+ *           p_j = exp(scale x_j - lse) is within about |lse| 2^-24 of itself.
  *   adjLogp, adjEntropy  [in] device fp32 [rows], or NULL for zero.  A row without a
  *           token takes no adjLogp.
  *   adjX    [out] device [rows, vocab] of dtype, leading dimension ldax; may be x

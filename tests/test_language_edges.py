@@ -97,3 +97,59 @@ def test_states_that_forget_at_once(batch, length, dim, groups, states, dtype):
     s["A"][0, 0] = math.nan
     y2, last2, _ = scan_forward(s)
     assert torch.isnan(y2[:, :, 0]).all() and torch.isnan(last2[:, 0, 0]).all() and torch.equal(last2[:, 1:], last[:, 1:])
+
+
+# ------------------------------------------------------- log probabilities ----
+
+def logit_inputs(rows, vocab, dtype, seed=0, std=3.0):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(rows, vocab, generator=g) * std).to(dtype)
+    tokens = torch.randint(0, vocab, (rows,), generator=g)
+    gl, ge = torch.randn(rows, generator=g), torch.randn(rows, generator=g)
+    return x.cuda(), tokens.cuda(), gl.cuda(), ge.cuda()
+
+
+def check_logp(x, tokens, scale, top, what):
+    """logp and top_logp to what their own size needs: the sum relative to the maximum, its logarithm, and the distance
+    from the maximum; no rounding of lse."""
+    import differentiable_cholesky_amd as dc
+    got = dc.chol_token_logprob(x, tokens, scale=scale, top=top)
+    y = x.double() * scale
+    d = y - y.amax(1, keepdim=True)
+    p = torch.exp(d)
+    log_s = torch.log(p.sum(1, keepdim=True))
+    p = p / p.sum(1, keepdim=True)
+    # a term is off by its exponent's size (3 U of it), the sum by its depth (lanes, waves, chunks); the logarithm by 2 U
+    # and 2 U of itself; the distance by two roundings of its own, the result by one
+    sum_err = (p * (3 * d.clamp(min=-1e4).abs() + 64 + 24)).sum(1, keepdim=True) * tu.U
+    bound = lambda far: sum_err + 2 * tu.U * (1 + log_s) + 2 * tu.U * far.abs() + tu.U * (far - log_s).abs()  # noqa: E731
+    far = d.gather(1, tokens[:, None])
+    tu.near(got.logp[:, None], far - log_s, bound(far), what + " logp")
+    assert (got.logp <= 0).all()
+    if top:
+        far = d.gather(1, got.top_ids)
+        tu.near(got.top_logp, far - log_s, bound(far), what + " top")
+        assert (got.top_logp <= 0).all() and (got.top_logp[:, 0] >= got.logp).all()
+
+
+LOGITS = [(300, 40), (200, 1000), (100, 5003), (20, 40000), (600, 20000), (3, 131072)]
+
+
+@pytest.mark.parametrize("scale", [0.7, 1.0, 1.5])
+@pytest.mark.parametrize("rows,vocab", LOGITS)
+def test_near_certain_tokens_have_no_positive_log_probability(rows, vocab, scale):
+    x, tokens, _, _ = logit_inputs(rows, vocab, torch.float32, seed=vocab, std=1.0)
+    x[torch.arange(rows), tokens] = 20 + 40 * torch.rand(rows, generator=torch.Generator().manual_seed(1)).cuda()
+    check_logp(x, tokens, scale, min(vocab, 5), "certain")
+
+
+@pytest.mark.parametrize("offset", [-2.0 ** 13, 1024.0, 2.0 ** 16])
+@pytest.mark.parametrize("rows,vocab", LOGITS)
+def test_an_offset_of_a_row_changes_no_log_probability(rows, vocab, offset):
+    import differentiable_cholesky_amd as dc
+    x, tokens, _, _ = logit_inputs(rows, vocab, torch.float32, seed=vocab)
+    x = torch.round(x * 64) / 64                                     # (so that the sum is exact)
+    check_logp(x + offset, tokens, 1.5, min(vocab, 8), "offset")
+    a, b = (dc.chol_token_logprob(t, tokens, scale=1.5, top=min(vocab, 8)) for t in (x, x + offset))
+    for k in ("logp", "entropy", "top_ids", "top_logp"):
+        assert torch.equal(getattr(a, k), getattr(b, k)), k
