@@ -4,7 +4,6 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 #include <cstdint>
 
 #include "../../include/libchol.h"
@@ -414,7 +413,8 @@ chol_status logprob_sizes(chol_dtype dt, int64_t rows, int64_t vocab)
     return CHOL_OK;
 }
 
-bool scale_ok(float scale) { return scale > 0.f && std::isfinite(scale); }
+// (the kernels multiply half distances by twice the scale and log2(e))
+bool scale_ok(float scale) { return scale > 0.f && scale <= 0x1p126f; }
 
 } // namespace
 

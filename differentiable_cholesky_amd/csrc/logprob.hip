@@ -115,21 +115,25 @@ __device__ __forceinline__ Entry wave_first(Entry e)
     return {key, wave_min(e.key == key ? e.index : INT_MAX)};
 }
 
-// A row's statistics, or a chunk's: its maximum, sum e and sum (x - m) e, with e =
-// 2^((x - m) k).  Without a value above -inf: -inf, 0, 0.
+// A row's statistics, or a chunk's: its maximum, sum e and sum g e, with e = 2^g and g =
+// (x - m) scale log2(e).  Without a value above -inf: -inf, 0, 0.
 struct Stats {
     float m, s, t;
 };
 
-// t, relative to a maximum d above (d < 0; e = 2^(d k), where it is 0 d may be anything).
-__device__ __forceinline__ float shifted(const Stats &st, float d, float e) { return e == 0.f ? 0.f : fmaf(d, st.s, st.t) * e; }
+// Half the distance to the maximum: the whole one, like a sum of distances instead of
+// exponents, may pass the largest number where a small scale makes little of it.
+__device__ __forceinline__ float half_below(float x, float m) { return fmaf(x, 0.5f, -0.5f * m); }
+
+// t, relative to a maximum above, from which g leads to its own (where e = 2^g is 0, g may be anything).
+__device__ __forceinline__ float shifted(const Stats &st, float g, float e) { return e == 0.f ? 0.f : fmaf(g, st.s, st.t) * e; }
 
 // Natural logarithm of the sum, and of a logit's probability.  The latter from the distance to the
 // maximum: from lse, whose rounding grows with the logits, a likely token's could come out above 0.
 __device__ __forceinline__ float log_sum(const Stats &st) { return __builtin_amdgcn_logf(st.s) * LN2; }
 __device__ __forceinline__ float log_prob(float scale, const Stats &st, float x)
 {
-    return x == -INFINITY && st.s == st.s ? x : fmaf(scale, x - st.m, -log_sum(st));
+    return x == -INFINITY && st.s == st.s ? x : fmaf(2.f * scale, half_below(x, st.m), -log_sum(st));
 }
 
 __device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stats st, float given)
@@ -140,7 +144,7 @@ __device__ __forceinline__ void finish(const LogprobArgs &a, int64_t row, Stats 
     const int64_t token = a.tokens[row];
     a.logp[row] = token < 0 || token >= a.vocab ? 0.f : log_prob(a.scale, st, given);
     if (a.entropy)
-        a.entropy[row] = st.m == -INFINITY && st.s == st.s ? 0.f : log_s - a.scale * (st.t / st.s);
+        a.entropy[row] = st.m == -INFINITY && st.s == st.s ? 0.f : log_s - LN2 * (st.t / st.s);
 }
 
 template <typename T> __device__ __forceinline__ float given_logit(const LogprobArgs &a, int64_t row)
@@ -180,7 +184,7 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
             x[i] = load_some<T, V>(p + c, end - c, (T)-INFINITY);
         }
     }
-    const float k2 = a.scale * LOG2E;
+    const float k = 2.f * a.scale * LOG2E; // (of half a distance)
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -195,9 +199,9 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float d = (float)x[i][v] - ref, e = __builtin_amdgcn_exp2f(d * k2);
+            const float g = half_below((float)x[i][v], ref) * k, e = __builtin_amdgcn_exp2f(g);
             s += e;
-            w = fmaf(fmaxf(d, -__FLT_MAX__), e, w); // (e is 0 at -inf)
+            w = fmaf(fmaxf(g, -__FLT_MAX__), e, w); // (e is 0 at -inf)
         }
     const float lane_sum = s;
     s = wave_sum(s), w = wave_sum(w);
@@ -320,9 +324,9 @@ __global__ void __launch_bounds__(THREADS) k_logprob(LogprobArgs a, int chunks, 
         for (int i = 0; i < TEAM; ++i) {
             const Stats o = s_stats[i];
             if (o.m > -INFINITY || o.s != o.s) {
-                const float d = o.m - all.m, e = __builtin_amdgcn_exp2f(d * k2);
+                const float g = half_below(o.m, all.m) * k, e = __builtin_amdgcn_exp2f(g);
                 all.s = fmaf(o.s, e, all.s);
-                all.t += shifted(o, d, e);
+                all.t += shifted(o, g, e);
             }
         }
     }
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(WAVE) k_logprob_join(LogprobArgs a, int chunks
     const int64_t row = blockIdx.x;
     for (int i = lane; i < chunks * a.top; i += WAVE)
         s_lists[i] = lists[row * chunks * a.top + i];
-    const float k2 = a.scale * LOG2E, given = given_logit<T>(a, row);
+    const float k = 2.f * a.scale * LOG2E, given = given_logit<T>(a, row);
     Stats st{-INFINITY, 0.f, 0.f};
     if (lane < chunks)
         st = stats[row * chunks + lane];
@@ -397,9 +401,9 @@ __global__ void __launch_bounds__(WAVE) k_logprob_join(LogprobArgs a, int chunks
     all.m = wave_max(st.m);
     float s = 0.f, t = 0.f;
     if (st.m > -INFINITY || st.s != st.s) {
-        const float d = st.m - all.m, e = __builtin_amdgcn_exp2f(d * k2);
+        const float g = half_below(st.m, all.m) * k, e = __builtin_amdgcn_exp2f(g);
         s = st.s * e;
-        t = shifted(st, d, e);
+        t = shifted(st, g, e);
     }
     all.s = wave_sum(s), all.t = wave_sum(t);
     if (lane == 0)

@@ -780,7 +780,7 @@ int64_t chol_selective_scan_block(int64_t states);
  *     lse = log sum_j exp(scale x_j),   logp = scale x_token - lse,
  *     entropy = -sum_j p_j log p_j,   p_j = exp(scale x_j - lse).
  *   dtype   CHOL_F32, CHOL_BF16 or CHOL_F16, of the logits.
- *   scale   positive and finite (the inverse of a temperature).
+ *   scale   positive, at most 2^126 (the inverse of a temperature).
  *   x       [in]  device [rows, vocab], leading dimension ldx.
  *   tokens  [in]  device int64 [rows]; outside 0 .. vocab-1 a row has no token
  *           and its logp is 0.

@@ -153,3 +153,28 @@ def test_an_offset_of_a_row_changes_no_log_probability(rows, vocab, offset):
     a, b = (dc.chol_token_logprob(t, tokens, scale=1.5, top=min(vocab, 8)) for t in (x, x + offset))
     for k in ("logp", "entropy", "top_ids", "top_logp"):
         assert torch.equal(getattr(a, k), getattr(b, k)), k
+
+
+@pytest.mark.parametrize("rows,vocab", [(5, 60), (3, 5000), (2, 40000), (600, 20000)])
+def test_extreme_scales(rows, vocab):
+    """Logits whose differences, or the sum of them, pass the largest number of their type, under scales that bring them
+    back; and scales near the largest."""
+    import differentiable_cholesky_amd as dc
+    x, tokens, _, _ = logit_inputs(rows, vocab, torch.float32, seed=vocab, std=1.0)
+    x = x.clamp(-3.9, 3.9)
+    want = dc.chol_token_logprob(x, tokens, scale=1.0, top=4)
+    for power in (-126, -120, -100, 60, 100):
+        # y is the same whatever the power: at -126 the logits reach 3.9 2^126 and their differences twice that; at 100 the
+        # least of them are still normal numbers
+        got = dc.chol_token_logprob(x * 2.0 ** -power, tokens, scale=2.0 ** power, top=4)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), power
+    flat = torch.zeros_like(x)
+    flat[:, ::2] = -2.0 ** 120
+    got = dc.chol_token_logprob(flat, tokens, scale=2.0 ** -120)
+    same = dc.chol_token_logprob(flat * 2.0 ** -120, tokens)
+    assert all(torch.equal(a, b) for a, b in zip(got[:3], same[:3])) and torch.isfinite(got.entropy).all()
+    assert (dc.chol_token_logprob(x, tokens, scale=2.0 ** 126).logp <= 0).all()
+    for scale in (2.0 ** 126.5, 3.4e38):
+        with pytest.raises(dc.CholError):
+            dc.chol_token_logprob(x, tokens, scale=scale)
