@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(THREADS) k_logprob_adjoint(LogprobAdjArgs a, u
         const int c = c0 + (i * lanes + t) * V;
         in[i] = load_some<T, V>(x + c, a.vocab - c);
     }
-    const bool empty = lse == -INFINITY; // no token is possible: zeros
+    // no token is possible, or no gradient reaches the row, whose logits may be anything: zeros
+    const bool empty = lse == -INFINITY || (gl == 0.f && ge == 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = c0 + (i * lanes + t) * V;

@@ -818,7 +818,9 @@ chol_status chol_token_logprob_workspace_size(chol_dtype dtype, int64_t rows, in
  *   adjLogp, adjEntropy  [in] device fp32 [rows], or NULL for zero.  A row without a
  *           token takes no adjLogp.
  *   adjX    [out] device [rows, vocab] of dtype, leading dimension ldax; may be x
- *           itself.  Zero in a row whose lse is -inf.
+ *           itself.  Zero in a row whose lse is -inf, and in one that takes no
+ *           gradient (adjLogp, or its token, and adjEntropy zero or none), whatever
+ *           its logits hold.
  */
 chol_status chol_token_logprob_adjoint(chol_dtype dtype, int64_t rows, int64_t vocab, const void *x, int64_t ldx,
                                        const int64_t *tokens, float scale, const float *lse, const float *entropy,

@@ -178,3 +178,27 @@ def test_extreme_scales(rows, vocab):
     for scale in (2.0 ** 126.5, 3.4e38):
         with pytest.raises(dc.CholError):
             dc.chol_token_logprob(x, tokens, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,vocab", [(9, 60), (6, 3001), (5, 70000)])
+def test_rows_that_take_no_gradient_have_none(rows, vocab, dtype):
+    """Padding's rows hold anything: with no token, or a weight of zero, and no gradient of the entropy they are zero."""
+    import differentiable_cholesky_amd as dc
+    x, tokens, gl, ge = logit_inputs(rows, vocab, dtype, seed=3)
+    clean = dc.chol_token_logprob(x, tokens)
+    want = dc.chol_token_logprob_adjoint(x, tokens, clean.lse, adjLogp=gl, entropy=clean.entropy, adjEntropy=ge)
+    only = dc.chol_token_logprob_adjoint(x, tokens, clean.lse, adjLogp=gl)
+    x[0], x[1, 5], x[2, vocab - 1] = math.nan, math.inf, math.nan
+    tokens[0], tokens[1] = -1, vocab
+    gl[2] = 0.0
+    ge[:3] = 0.0
+    got = dc.chol_token_logprob(x, tokens)
+    assert torch.isnan(got.lse[:3]).all()
+    d = dc.chol_token_logprob_adjoint(x, tokens, got.lse, adjLogp=gl, entropy=got.entropy, adjEntropy=ge)
+    assert not d[:3].any() and torch.equal(d[3:], want[3:])
+    d = dc.chol_token_logprob_adjoint(x, tokens, got.lse, adjLogp=gl)
+    assert not d[:3].any() and torch.equal(d[3:], only[3:])
+    # one that takes a gradient has what its definition has
+    gl[2] = 1.0
+    assert torch.isnan(dc.chol_token_logprob_adjoint(x, tokens, got.lse, adjLogp=gl)[2]).all()
