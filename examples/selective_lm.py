@@ -110,9 +110,9 @@ class SelectiveLM:
         g["embed"].copy_(embed.index_add_(0, tokens.reshape(-1), ds.float()))
 
     def loss(self, tokens, bonus=0.0):
-        """Mean negative log probability of [batch, len + 1] tokens' next ones (below zero: none), less
-        ``bonus`` times the mean entropy; gradients into self.g."""
-        logits, kept = self.forward(tokens[:, :-1])
+        """Mean over all places of the negative log probability of [batch, len + 1] tokens' next ones (below
+        zero, padding: none, which counts as 0), less ``bonus`` times the mean entropy; gradients into self.g."""
+        logits, kept = self.forward(tokens[:, :-1].clamp(min=0))     # (padding is read as token 0)
         want = tokens[:, 1:].reshape(-1)
         r = dc.chol_token_logprob(logits, want)
         weight = torch.full_like(r.logp, -1.0 / len(want))
