@@ -6,7 +6,7 @@
 //   adj_x_j = scale (gl (1[j = token] - p_j) - ge p_j (log p_j + entropy)),  p = e^(y - lse)
 //
 // Memory bounds both: forward reads a row once, the adjoint reads and writes it once
-// (4096 x 128000 bf16 173 us, 6.1 TB/s, and 398 us, 5.3 TB/s).  A
+// (4096 x 128000 bf16 175 us, 6.0 TB/s, and 399 us, 5.3 TB/s).  A
 // row is cut into chunks that stay in the registers of a wave (short rows, four to a
 // workgroup) or of a workgroup, so that the maximum, the sums relative to it and the
 // search for alternatives take one reading.  Several chunks a row (long rows, or few of
@@ -15,13 +15,14 @@
 // Alternatives: the k-th largest maximum of a lane is a bound that k elements reach, so only
 // lanes that reach it, hardly more than k of the workgroup, can hold one.  Their elements go
 // through LDS, a lane an element; those that reach the bound are ranked against each other
-// (4096 x 128000 bf16 with 1, 8 and 20 alternatives 191, 244 and 293 us, where the search's own
+// (4096 x 128000 bf16 with 1, 8 and 20 alternatives 190, 243 and 296 us, where the search's own
 // vector instructions and barriers add to a kernel that fills three quarters of the units; a
 // bound and a list for each wave, found by comparing all lanes, took 221, 291 and 415, and
 // comparing every element in its own lane 896 for 8).  Where lanes or elements are too many
-// (equal values, sorted rows) a wave finds each
-// alternative in turn among its elements, k times the comparisons.  Order: by value, then by
-// the lower index; NaN before all.
+// (equal values, sorted rows, or fewer lanes with a column above -inf than alternatives, so that
+// the bound is -inf) a wave finds each alternative in turn among its elements, k times the
+// comparisons (with 50 columns of 128000 above -inf 8 alternatives take 5090 us, 20 12500; 16
+// rows 38 for 18).  Order: by value, then by the lower index; NaN before all.
 #include <algorithm>
 #include <climits>
 #include <type_traits>

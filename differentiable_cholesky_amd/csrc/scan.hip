@@ -8,9 +8,10 @@
 // (measured), 93 us for 4 x 2048 x 4096 of 16 states, where the channels' four 16-bit
 // numbers take 52 of memory.  So the vector units bound it, and the layout (scan_lanes.hpp)
 // serves them.  4 x 2048 x 4096 bf16 of 16 states, saving states: 182 us, one wave a SIMD,
-// which issues an instruction in 86 of 100 cycles: of 480 vector instructions a wave and 16
+// whose vector instructions take 69 of 100 cycles: of 480 vector instructions a wave and 16
 // steps 320 are the walk, 90 softplus, 80 the gate, the sums over rows and the stores.  8 x 4096 x
-// 4096 570 us.  1 x 16384 x 4096 437 us: 16 segments, a first walk of 207.
+// 4096 574 us.  1 x 16384 x 4096 442 us: 16 segments, of which a first walk takes 40 % (traced by
+// themselves 213 and 314 us).
 #include "scan_lanes.hpp"
 
 namespace chol {

@@ -12,7 +12,7 @@
 // Sums over the channels take the lanes of a row, the waves of the workgroup, and by a last
 // launch the workgroups.
 //
-// Vector instructions bound it (890 a wave and 8 steps of 16 states, of which 160 walk up
+// Vector instructions bound it (900 a wave and 8 steps of 16 states, of which 160 walk up
 // to the parts, 500 walk down, half of that the sums over lanes and rows), with two waves a
 // SIMD, which 225 registers a lane and 74 KB of LDS a workgroup leave room for.  4 x 2048 x 4096
 // bf16 of 16 states 630 us: first walks 95, walks 520, sums 12; 8 x 2048 x 4096 1090 us.

@@ -269,7 +269,8 @@ Plan plan_of(const ScanArgs &a, bool adjoint)
     const int64_t per = a.dim / a.groups, wave_count = (per + ROW - 1) / ROW, block = scan_block(a.states);
     // Waves of a workgroup lie along a group's channels; the adjoint's idle ones would wait
     // at its barriers, so it takes one or two where a group has no more (27 x 1863 x 16 of 4
-    // groups of 64 states 1250 -> 490 us, 27 x 2530 x 76 of 4 groups of 11 366 -> 271).
+    // groups of 64 states 1250 -> 490 us, 27 x 2530 x 76 of 4 groups of 11 366 -> 271).  Beyond
+    // that it has four, up to three of them idle in a group's last workgroup.
     const int waves = p.waves = adjoint && wave_count <= 2 ? (int)wave_count : WAVES;
     p.per_group = (int)((wave_count + waves - 1) / waves);
     p.across = (int64_t)p.per_group * a.groups;
@@ -277,7 +278,7 @@ Plan plan_of(const ScanArgs &a, bool adjoint)
     // which also needs two waves a SIMD more: 4 x 2048 x 4096 bf16 (1024 waves, one a
     // SIMD) forward 178 us whole, 219 in 4 segments, adjoint 900 and 721; 2 x 2048 x 4096 forward
     // 160 in 2 segments, 126 in 8, adjoint 576 and 368.  Beyond 32 states a SIMD holds one wave,
-    // and segments only fill it (4 x 2048 x 4096 of 64 states adjoint 2790 us whole, 3100 in 4;
+    // and segments only fill it (4 x 2048 x 4096 of 64 states adjoint 2790 us whole, 3100 in 4 at the time;
     // 16 x 416 x 71 forward 43 us in 7, 73 in 26, adjoint 118 in 7, 162 in 9).  More than 64 segments cost more to put together than they save (16384 x 256
     // forward 68 us, with 256 116).
     // (waves, with the idle ones: they hold a place)

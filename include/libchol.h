@@ -668,7 +668,8 @@ chol_status chol_causal_conv(chol_dtype dtype, int silu, int64_t batch, int64_t 
  *   adjState  [out] gradient of state, [batch, width - 1, dim], or NULL.
  * Outputs share no element with inputs or each other.
  *   workspace at least chol_causal_conv_adjoint_workspace_size bytes (4-byte
- *             aligned; NULL allowed when it is 0).
+ *             aligned; NULL allowed when it is 0): 4 (width + 1) dim for every
+ *             workgroup along batch and sequence, at least batch of them.
  */
 chol_status chol_causal_conv_adjoint(chol_dtype dtype, int silu, int64_t batch, int64_t len, int64_t dim, int64_t width,
                                      const void *x, int64_t ldx, int64_t strideX,
@@ -752,7 +753,9 @@ typedef struct {
 /*
  * chol_selective_scan, chol_selective_scan_adjoint -- the scan of chol_scan_args,
  * and its adjoint.  workspace: at least as many bytes as the _workspace_size
- * call gives (4-byte aligned; NULL allowed when it is 0).
+ * call gives (4-byte aligned; NULL allowed when it is 0).  The adjoint's has 128
+ * bytes (256, 512 beyond 16, 32 states) for every step, batch element and 64
+ * channels of a group, as much as a 16-bit [batch, len, dim] array at up to 16.
  * states above CHOL_SCAN_MAX_STATES, len above 2^30, batch * dim * states above
  * 2^31 - 1, rows of one sequence more than 2^25 elements apart, and sizes that need
  * 2^32 threads or more, return CHOL_ERR_NOT_SUPPORTED; groups that do not divide dim
