@@ -68,6 +68,25 @@ def test_an_infinite_entry_of_the_last_row(batch, length, dim, groups, states):
         assert torch.equal(got[k][:, :-1], clean[k][:, :-1]) and torch.equal(got[k][1:], clean[k][1:]), k
 
 
+@pytest.mark.parametrize("batch,length,dim,groups,states", [c for c in ODD if c[1] <= 90])
+def test_an_infinite_weight_of_the_last_row(batch, length, dim, groups, states):
+    """C infinite in the last step: the gradient of that state is infinite all the way to the first, those of the others
+    are as they were."""
+    s = scan_inputs(batch, length, dim, groups, states, seed=length)
+    _, last, starts = scan_forward(s, save=True)
+    clean = scan_adjoint(s, starts)["h0"]
+    n = states // 2
+    s["C"][0, -1, groups - 1, n] = math.inf
+    _, last2, starts2 = scan_forward(s, save=True)
+    assert torch.equal(last2, last) and torch.equal(starts2, starts)
+    got = scan_adjoint(s, starts2)["h0"]
+    hit = torch.arange(dim, device="cuda") // (dim // groups) == groups - 1
+    # (silu has the sign of z; these states' steps are short enough that no exponential, of a segment neither, is 0)
+    assert torch.equal(got[0, hit, n], (s["adj"][0, -1, hit] * s["z"][0, -1, hit]).sign() * math.inf)
+    got[0, hit, n] = clean[0, hit, n]
+    assert torch.equal(got, clean)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("batch,length,dim,groups,states", ODD)
 def test_states_that_forget_at_once(batch, length, dim, groups, states, dtype):
